@@ -414,6 +414,139 @@ int sbsa_prefill_noalloc(const sbsa_params* p, const void* q, const void* k, con
                          const void* q_idx, const void* k_idx, void* o, int32_t* idx_out,
                          int32_t* cnt_out, uint8_t* flags_out, void* stream);
 
+/*
+ * The 4-bit key-value cache: what a prefill leaves behind for generation, in
+ * pages of 4-bit keys and values.  The pages of the sources above stop at
+ * the prefill and have no cache; the operators, the format and the layout
+ * are this library's.
+ *
+ * Format.  The d channels of one token's key (or value) of one kv head fall
+ * into groups of 32.  A group holds
+ *   low    bf16: the group's least value rounded down to bf16 (-0 as +0),
+ *   scale  bf16: (largest value - low) * (1/15 in fp32), each step in fp32,
+ *          then rounded up to bf16, so that 15 steps reach the largest value;
+ *          0 when largest - low < 2^-100 (a constant group),
+ *   level  4 bits a channel: rint((x - low) * (1/scale)) in fp32, at most 15,
+ * and a channel stands for low + scale * level (one rounding in fp32).  A
+ * group that holds a NaN or an infinity, or whose range overflows fp32 or
+ * bf16, stands for NaN throughout.  A token takes 5/8 d bytes for its key and
+ * as many for its value, per kv head.
+ *
+ * Layout.  cache: device uint8 [n_pages, Hkv, 2, page_size * 5d/8], 16-byte
+ * aligned, keys at index 0 and values at index 1 of the third axis.  The last
+ * axis holds the levels of the page's tokens, [page_size, d/2], then their
+ * pairs (scale, low), [page_size, d/32, 2] bf16.  Within a token's d/2 bytes
+ * (the low half of a byte is the even channel) the channels stand in the
+ * order in which the attention's matrix fragments take them:
+ *   key    channel 32 g + 8 q + i (q < 4, i < 8): byte q d/8 + 4 g + i/2;
+ *   value  channel 32 g + 4 r + i (r < 8, i < 4): byte r' d/16 + 2 g + i/2,
+ *          r' = r, but r ^ 4 at d = 128 in the tokens of a page whose number
+ *          has bit 1 set (so that a warp's reads meet no bank twice).
+ *
+ * A batch.  All three operators take the same description of n_seqs sequences:
+ *   page_table device int32 [n_seqs, max_pages]: token t of sequence b lies in
+ *              page page_table[b, t / page_size], at t % page_size; entries
+ *              behind a sequence's last page are not read.  Sequences may
+ *              share pages that they only read.
+ *   seq_lens   device int32 [n_seqs]: tokens of the sequence, the new ones counted.
+ *   cu_new     device int32 [n_seqs + 1], ascending: rows cu_new[b] to
+ *              cu_new[b + 1] - 1 of k, v, q and o are the last tokens of sequence
+ *              b: row cu_new[b + 1] - 1 is token seq_lens[b] - 1.  A sequence may
+ *              have none.  Rows before cu_new[0] and from cu_new[n_seqs] on are
+ *              left as they are.
+ * None of it is read by the host: lengths and tables may change between the
+ * replays of a captured graph.  What is out of range there (a page number
+ * outside [0, n_pages), a length beyond the table, a row of a token before the
+ * sequence's first) is skipped as said at each operator and reported as
+ * SBSA_ERR_DEVICE through sbsa_get_status.
+ * Pointers and strides belong to the current device.  n_seqs = 0 or
+ * n_tokens = 0 enqueues nothing.
+ */
+typedef struct sbsa_kv4_params {
+  int n_q_heads;   /* attend: Hq, a multiple of n_kv_heads; else ignored         */
+  int n_kv_heads;  /* Hkv >= 1 (at most 65535)                                   */
+  int head_dim;    /* d in {64, 128}                                             */
+  int page_size;   /* tokens of a page: 16, 32, 64 or 128                        */
+  int n_pages;     /* pages in the cache, >= 1                                   */
+  int max_pages;   /* width of the page table, >= 1                              */
+  int n_seqs;      /* >= 0                                                       */
+  int n_tokens;    /* rows of k, v, q, o per head, >= 0                          */
+  int max_new;     /* attend: at least the most rows of one sequence, >= 1; rows
+                      beyond it are not computed and reported as SBSA_ERR_DEVICE */
+  int dtype;       /* SBSA_BF16 | SBSA_FP32: of k, v, q, o                       */
+  int list_heads;  /* attend: 0 without lists; else Hkv (one list per kv head)
+                      or Hq (one per query head)                                 */
+  int block_size;  /* with lists: tokens of a listed block, 64 or 128, a
+                      multiple of page_size                                      */
+  int max_blocks;  /* with lists: width of idx, >= 1                             */
+  float sm_scale;  /* attend: logit scale; 0 => 1/sqrt(head_dim)                 */
+} sbsa_kv4_params;
+
+/* Bytes of a cache of these parameters; 0 when they are invalid. */
+size_t sbsa_kv4_cache_bytes(const sbsa_kv4_params* p);
+
+/*
+ * sbsa_kv4_append -- quantise new keys and values into the cache.
+ *   k, v      device [Hkv, n_tokens, d] of p->dtype, 16-byte aligned, with strides
+ *             in elements between tokens and between heads (multiples of 16
+ *             bytes; [n_tokens, Hkv, d] projections are taken as they are).
+ *   k_stored, v_stored  device [Hkv, n_tokens, d] contiguous of p->dtype, or
+ *             NULL: what the cache now stands for, rounded to p->dtype (for a
+ *             prompt's own attention to see the values that later tokens see).
+ * Writes the rows' tokens and nothing else of the cache; a row whose token is
+ * out of range is skipped (and left in k_stored and v_stored).  Two sequences
+ * that append to one place of the cache leave it undefined.
+ * Errors: SBSA_ERR_INVALID_ARG for null or misaligned pointers, inconsistent
+ * parameters or strides; SBSA_ERR_UNSUPPORTED for other d or page_size;
+ * SBSA_ERR_CUDA on a launch failure.
+ */
+int sbsa_kv4_append(const sbsa_kv4_params* p, void* cache, const int32_t* page_table,
+                    const int32_t* seq_lens, const int32_t* cu_new, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                    int64_t v_token_stride, int64_t v_head_stride, void* k_stored,
+                    void* v_stored, void* stream);
+
+/*
+ * sbsa_kv4_read -- the same rows back from the cache: with cu_new the running
+ * sum of seq_lens, whole sequences.
+ *   k_out, v_out  device [Hkv, n_tokens, d] contiguous of p->dtype (the layout of
+ *             sbsa_pool_blocks, sbsa_prefill), 16-byte aligned; either may be NULL.
+ * A row whose token is out of range reads as zeros.  Errors as sbsa_kv4_append.
+ */
+int sbsa_kv4_read(const sbsa_kv4_params* p, const void* cache, const int32_t* page_table,
+                  const int32_t* seq_lens, const int32_t* cu_new, void* k_out, void* v_out,
+                  void* stream);
+
+/* Device workspace of sbsa_kv4_attend: partial results of the rows whose
+ * tokens are shared out over several CTAs.  0 when p is invalid. */
+size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
+
+/*
+ * sbsa_kv4_attend -- attention of new tokens over the cache (which holds them
+ * already: append first), exact softmax.
+ *   q, o      device [Hq, n_tokens, d] of p->dtype, 16-byte aligned, with strides in
+ *             elements between tokens and between heads (multiples of 16 bytes).
+ *   idx, cnt  with p->list_heads: device int32 [n_seqs, list_heads, max_blocks] and
+ *             [n_seqs, list_heads], as sbsa_select writes them: row (b, h) lists
+ *             cnt blocks of p->block_size tokens of sequence b.  NULL without.
+ *   workspace device, 256-byte aligned, ws_bytes >= sbsa_kv4_attend_workspace_bytes(p);
+ *             nothing in it is kept between calls.  Calls that may overlap on
+ *             the GPU need one each.
+ * o of row t (token position n of sequence b) = sum over the tokens u <= n, of
+ * the listed blocks if there are lists, of softmax_u(q . K[u] * sm_scale) V[u],
+ * where query head h reads kv head h / (Hq / Hkv); a row that sees no token is
+ * 0.  Listed blocks outside the sequence, pages outside the cache, and rows out
+ * of range are skipped (o is 0 there) and reported as SBSA_ERR_DEVICE; a
+ * repeated block is attended twice.
+ * Errors as sbsa_kv4_append, and SBSA_ERR_WORKSPACE for a missing, misaligned
+ * or short workspace.
+ */
+int sbsa_kv4_attend(const sbsa_kv4_params* p, const void* cache, const int32_t* page_table,
+                    const int32_t* seq_lens, const int32_t* cu_new, const void* q,
+                    int64_t q_token_stride, int64_t q_head_stride, void* o,
+                    int64_t o_token_stride, int64_t o_head_stride, const int32_t* idx,
+                    const int32_t* cnt, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
