@@ -45,7 +45,9 @@ namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kWarps = 8;                       // computing warps
-constexpr int kThreads = (kWarps + 1) * 32;     // and one that copies
+// and one that copies; with its three idle neighbours a warpgroup, whose registers the computing
+// warps take over
+constexpr int kThreads = (kWarps + 4) * 32;
 constexpr int kTile = 16;                       // tokens of a warp's step
 constexpr int kUnit = kWarps * kTile;           // tokens of a stage
 constexpr int kMaxCtas = 160;
@@ -300,7 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     if (p.a.b.status) atomicCAS(p.a.b.status, 0, SBSA_ERR_TIMEOUT);
   };
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
+    regs_lower<56>();
+    if (warp > kWarps) return;
     // ================================================================ copies
     const int pages = kUnit / page;
     int n = 0;  // stages filled
@@ -319,12 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
         count = clamp_int(p.a.cnt[row], 0, p.a.max_blocks);
       }
       const int32_t* table = p.a.b.table + (long long)w.b * p.a.b.max_pages;
-      // page number and first position of this lane's page of unit u
-      auto look = [&](int u, int* pos) {
-        int at = u * kUnit + lane * page;
-        if (lane >= pages) return -1;
+      // 32 pages at a time: lane x looks up page x (its number, or -1, and the position of its
+      // first token), so that a memory round trip serves 32 * page / 128 units
+      auto look = [&](int first, int* pos) {
+        long long at = (long long)(first + lane) * page;
+        *pos = INT_MAX - kUnit;
         if (list) {
-          const int e = at / p.a.block;
+          const int e = (int)(at / p.a.block);
           if (e >= count) return -1;
           const int j = list[e];
           if (j < 0 || j > (s.len - 1) / p.a.block || s.len == 0) {
@@ -333,37 +338,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
           }
           at = j * p.a.block + at % p.a.block;
         }
-        *pos = at;
         if (at >= limit) return -1;
         const int pg = table[at / page];
         if (pg < 0 || pg >= p.a.b.n_pages) {
           kv4_record(p.a.b.status);
           return -1;
         }
+        *pos = (int)at;
         return pg;
       };
-      int pos = 0, pg = look(w.at, &pos);
+      const uint8_t* heads = p.a.cache + (long long)(w.head / p.kv_div) * 2 * rec;
+      int chunk = w.at * pages, pos, pg = look(chunk, &pos);
       for (int u = w.at; u < end; ++u) {
-        int pos2 = 0, pg2 = -1;
-        if (u + 1 < end) pg2 = look(u + 1, &pos2);
+        if (u * pages - chunk + pages > 32) {
+          chunk = u * pages;
+          pg = look(chunk, &pos);
+        }
         const int st = n % C::kStages;
         bool good = true;
         if (lane == 0 && n >= C::kStages)
           good = mbar_wait_bounded(&empty[st], (n / C::kStages - 1) & 1, abort_flag, kTimeoutNs);
         ok = __shfl_sync(0xFFFFFFFFu, good, 0);
         if (!ok) break;
-        if (lane < pages) s_meta[st * 8 + lane] = pg < 0 ? INT_MAX - kUnit : pos;
-        const int bytes = 2 * rec * __popc(__ballot_sync(0xFFFFFFFFu, pg >= 0));
+        const int x = lane - (u * pages - chunk);  // this lane's page within the unit
+        const bool in = x >= 0 && x < pages;
+        if (in) s_meta[st * 8 + x] = pos;
+        const int bytes = 2 * rec * __popc(__ballot_sync(0xFFFFFFFFu, in && pg >= 0));
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
         __syncwarp();
-        if (pg >= 0)
-          bulk_load(smem + st * C::kStageBytes + lane * 2 * rec,
-                    p.a.cache + ((long long)pg * p.a.b.hkv + w.head / p.kv_div) * 2 * rec,
-                    2 * rec, &full[st]);
+        if (in && pg >= 0)
+          bulk_load(smem + st * C::kStageBytes + x * 2 * rec,
+                    heads + (long long)pg * p.a.b.hkv * 2 * rec, 2 * rec, &full[st]);
         ++n;
-        pos = pos2;
-        pg = pg2;
       }
       w.left -= end - w.at;
       if (w.left > 0) next_item<ROWS>(p, w);
@@ -378,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   }
 
   // ==================================================================== products
+  regs_raise<224>();  // 256 * 224 + 128 * 56 = 384 * 168, what the block was launched with
   const int r = lane >> 2, q = lane & 3;
   // Column n of S is token n ^ (n >> 2) of 8: with it neither the keys', the
   // values' nor the pairs' reads meet a bank twice.  A lane's logits are those of
