@@ -44,35 +44,43 @@ namespace sbsa {
 namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kWarps = 8;                       // computing warps
-// and one that copies; with its three idle neighbours a warpgroup, whose registers the computing
-// warps take over
-constexpr int kThreads = (kWarps + 4) * 32;
-constexpr int kTile = 16;                       // tokens of a warp's step
-constexpr int kUnit = kWarps * kTile;           // tokens of a stage
+constexpr int kTile = 16;         // tokens of a warp's step
+constexpr int kUnit = 8 * kTile;  // tokens of a stage: 8 warps take it
 constexpr int kMaxCtas = 160;
-// P is exp2(S - M) with M at least (largest S + E) - kHead - kLazy, E the
-// exponent of the largest scale or low met: the fp16 weights P * scale stay below
-// 2^(kHead + kLazy + 1) = 2^15, and M moves only when S + E has outgrown it by kLazy.
-constexpr float kHead = 6.f, kLazy = 8.f;
+// Weights are 2^(S - M), M = (reference of the logits) + (reference of the
+// values' exponents) - kHead; each reference moves only when it is outgrown by more
+// than kLazy, so the fp16 weights times a scale stay below 2^(kHead + 2 kLazy + 1) = 2^15.
+constexpr float kHead = 6.f, kLazy = 4.f;
 
-template <int D, int NT>
+// W computing warps take the tiles of 16 tokens in turn.  8 bf16 rows leave
+// registers for 12; 16 rows or two-part fp32 rows take 8 (spilled registers cost
+// far more than warps gain: next to the ring the L1 has a few KB left).  The copying
+// warp and its three idle neighbours are a warpgroup whose registers the computing
+// warps take over.
+template <int D, int NT, int W>
 struct Cfg {
+  static constexpr int kWarps = W;
+  static constexpr int kThreads = (W + 4) * 32;
+  // launched with 128 (512 threads) or 168 (384) registers a thread: 384 * 152 + 128 * 56 =
+  // 512 * 128, 256 * 224 + 128 * 56 = 384 * 168
+  static constexpr int kRegs = W == 12 ? 152 : 224, kRegsCopy = 56;
   static constexpr int kRows = 8 * NT;
   static constexpr int kGroups = D / 32;
   static constexpr int kStageBytes = kUnit * (D / 8) * 10;
-  static constexpr int kStages = D == 64 ? 10 : (NT == 1 ? 8 : 7);
+  static constexpr int kStages = D == 64 ? 10 : 7;
   static constexpr int kOutStride = D + 4;  // floats; spreads the heads over the banks
   static constexpr int kOffOut = kStages * kStageBytes;
   static constexpr int kOffStat = kOffOut + kWarps * kRows * kOutStride * 4;
   // per warp and row: M, l, and the lows' sums of the groups
   static constexpr int kStat = 2 + kGroups;
-  static constexpr int kOffMeta = kOffStat + kWarps * kRows * kStat * 4;
+  // per warp: its tokens' key and value scales in fp32
+  static constexpr int kOffScale = kOffStat + kWarps * kRows * kStat * 4;
+  static constexpr int kOffMeta = kOffScale + kWarps * 2 * kTile * kGroups * 4;
   static constexpr int kOffScan = kOffMeta + kStages * 8 * 4;
   static constexpr int kOffBar = kOffScan + (kThreads / 32 + 1) * 8 + 32;
   static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
+  static_assert(kOffBar % 8 == 0 && kOffScan % 8 == 0 && kOffScale % 16 == 0, "alignment");
 };
 
 struct Part {  // which item's first part a CTA holds, in how many parts (0: none)
@@ -106,6 +114,10 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
   return s;
 }
 
+// What an item costs a CTA besides its units (rows, joining, output), in units.  Runs are
+// cut by cost: item after item, kItemCost and then the units.
+constexpr int kItemCost = 4;
+
 // Units of 128 tokens of each row tile of (sequence, head) and the number of
 // tiles; a tile that sees nothing still takes one unit (it writes zeros).
 template <int ROWS>
@@ -120,35 +132,80 @@ __device__ __forceinline__ void item_size(const Params& p, int b, int head, int*
   *units = n < 1 ? 1 : n;
 }
 
-// The CTA's place in the sequence of units.
+// The CTA's place in the sequence of items.
 struct Walk {
-  int b, head, tile;       // current item
-  int units, tiles;        // its units, its sequence's tiles
-  int at;                  // first unit to do
-  long long left;          // units left in the CTA's run
+  int b, head, tile;   // current item
+  int units, tiles;    // its units, its sequence's tiles
+  long long cost;      // cost from the item's start to the run's first
+  long long left;      // and to the run's end
+  // units of the item that are the CTA's: [begin, end), empty where the run ends before the first
+  __device__ int begin() const { return cost > kItemCost ? (int)cost - kItemCost : 0; }
+  __device__ int end() const {
+    const long long e = left - kItemCost;
+    return e < 0 ? 0 : e < units ? (int)e : units;
+  }
 };
+
+__device__ __forceinline__ long long units_cost(int units) { return (long long)kItemCost + units; }
 
 template <int ROWS>
 __device__ __forceinline__ void next_item(const Params& p, Walk& w) {
-  w.at = 0;
+  w.left -= units_cost(w.units);
+  w.cost = 0;
+  if (w.left <= 0) return;
   if (++w.tile < w.tiles) return;
   w.tile = 0;
   do {
     if (++w.head == p.heads) {
       w.head = 0;
-      if (++w.b == p.a.b.n_seqs) return;  // left is 0 by then
+      if (++w.b == p.a.b.n_seqs) {
+        w.left = 0;
+        return;
+      }
     }
     item_size<ROWS>(p, w.b, w.head, &w.units, &w.tiles);
   } while (w.tiles == 0);
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+// D += A B on fp16, 16 x 16 by 16 x 8; and D = A B.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D = A B on bf16.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D += A B on tf32, 16 x 8 by 8 x 8; rows 8 to 15 of A are zero.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
+}
+
+// Two fp32 values as their bf16 parts: returns the leading parts and leaves the rest.
+__device__ __forceinline__ uint32_t take_bf16(float& lo, float& hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+  lo -= __uint_as_float(w << 16);
+  hi -= __uint_as_float(w & 0xFFFF0000u);
+  return w;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -157,17 +214,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 __device__ __forceinline__ float scale_of(uint32_t pair) { return __uint_as_float(pair << 16); }
-__device__ __forceinline__ float low_of(uint32_t pair) {
-  return __uint_as_float(pair & 0xFFFF0000u);
-}
-
 // The words of one token's chunk of levels, or its pairs, for all groups.
 template <int NG>
 struct Words {
   uint32_t w[NG];
 };
 template <int NG>
-__device__ __forceinline__ Words<NG> lds_words(const unsigned char* p) {
+__device__ __forceinline__ Words<NG> lds_words(const void* p) {
   Words<NG> r;
   if constexpr (NG == 4) {
     const uint4 u = *reinterpret_cast<const uint4*>(p);
@@ -212,17 +265,20 @@ __device__ __forceinline__ bool row_of(const Params& p, const Seq& s, int head, 
   return true;
 }
 
+template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 // T: type of q and o.  fp32 rows enter the products as two fp16 parts (22
 // bits), and so do their weights; a bf16 row is one fp16 part exactly (its
 // elements are scaled by a power of two so that the largest is near 2^10) and
 // the weights are rounded to fp16 once, 2^-11 of each.
-template <int D, int NT, typename T>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<D, NT>;
+template <int D, int NT, int W, typename T>
+__global__ void __launch_bounds__((W + 4) * 32, 1)
+    kv4_attend_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, NT, W>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   constexpr int NG = C::kGroups;
   constexpr int ROWS = C::kRows;
   constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
@@ -246,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   for (int i = i0; i < i1; ++i) {
     int units, tiles;
     item_size<ROWS>(p, i / p.heads, i % p.heads, &units, &tiles);
-    mine += (long long)units * tiles;
+    mine += units_cost(units) * tiles;
   }
   long long incl = mine;
 #pragma unroll
@@ -258,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kWarps);
+      mbar_init(&empty[s], 8);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -281,29 +337,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     for (int i = i0; i < i1; ++i) {
       int units, tiles;
       item_size<ROWS>(p, i / p.heads, i % p.heads, &units, &tiles);
-      if (u0 < x + (long long)units * tiles) {
+      if (u0 < x + units_cost(units) * tiles) {
         s_start[0] = i / p.heads;
         s_start[1] = i % p.heads;
-        s_start[2] = (int)((u0 - x) / units);
-        s_start[3] = (int)((u0 - x) % units);
+        s_start[2] = (int)((u0 - x) / units_cost(units));
+        s_start[3] = (int)((u0 - x) % units_cost(units));
         break;
       }
-      x += (long long)units * tiles;
+      x += units_cost(units) * tiles;
     }
   }
   __syncthreads();
   Walk w;
-  w.b = s_start[0], w.head = s_start[1], w.tile = s_start[2], w.at = s_start[3];
-  w.left = u1 - u0;
+  w.b = s_start[0], w.head = s_start[1], w.tile = s_start[2], w.cost = s_start[3];
+  w.left = w.cost + u1 - u0;
   item_size<ROWS>(p, w.b, w.head, &w.units, &w.tiles);
 
+  float* ks = reinterpret_cast<float*>(smem + C::kOffScale) + warp * 2 * kTile * NG;
+  float* vs = ks + kTile * NG;
   auto fail = [&]() {
     *abort_flag = 1;
     if (p.a.b.status) atomicCAS(p.a.b.status, 0, SBSA_ERR_TIMEOUT);
   };
 
   if (warp >= kWarps) {
-    regs_lower<56>();
+    regs_lower<C::kRegsCopy>();
     if (warp > kWarps) return;
     // ================================================================ copies
     const int pages = kUnit / page;
@@ -311,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     bool ok = true;
     while (w.left > 0 && ok) {
       const Seq s = seq_of(p, w.b);
-      const int end = (int)min((long long)w.units, w.at + w.left);
+      const int begin = w.begin(), end = w.end();
       // tokens that the tile's last row sees
       const long long last = min((long long)(w.tile + 1) * ROWS, (long long)s.rows * p.group) - 1;
       const int limit = s.len - s.rows + (int)(last / p.group) + 1;
@@ -348,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
         return pg;
       };
       const uint8_t* heads = p.a.cache + (long long)(w.head / p.kv_div) * 2 * rec;
-      int chunk = w.at * pages, pos, pg = look(chunk, &pos);
-      for (int u = w.at; u < end; ++u) {
+      int chunk = begin * pages, pos = 0, pg = begin < end ? look(chunk, &pos) : -1;
+      for (int u = begin; u < end; ++u) {
         if (u * pages - chunk + pages > 32) {
           chunk = u * pages;
           pg = look(chunk, &pos);
@@ -372,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
                     heads + (long long)pg * p.a.b.hkv * 2 * rec, 2 * rec, &full[st]);
         ++n;
       }
-      w.left -= end - w.at;
-      if (w.left > 0) next_item<ROWS>(p, w);
+      next_item<ROWS>(p, w);
     }
     if (!ok && lane == 0) {
       if (!*abort_flag) fail();
@@ -385,24 +442,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   }
 
   // ==================================================================== products
-  regs_raise<224>();  // 256 * 224 + 128 * 56 = 384 * 168, what the block was launched with
+  regs_raise<C::kRegs>();
   const int r = lane >> 2, q = lane & 3;
   // Column n of S is token n ^ (n >> 2) of 8: with it neither the keys', the
   // values' nor the pairs' reads meet a bank twice.  A lane's logits are those of
   // columns 2q and 2q + 1, its key rows' that of column r.
   const int tok_k = r ^ (r >> 2);
   const int tok_a = (2 * q) ^ (q >> 1), tok_b = (2 * q + 1) ^ (q >> 1);
-  int n = 0;
+  // this warp's next tile (8 to a stage), and its stage's number and place in the ring
+  int tile = warp, stage = 0, st = 0, phase = 0;
+  int base_n = 0;                    // the number of the item's first stage
   bool ok = true;
   while (w.left > 0) {
     const Seq s = seq_of(p, w.b);
-    const int begin = w.at, end = (int)min((long long)w.units, w.at + w.left);
+    const int begin = w.begin(), end = w.end();
+    if (begin >= end) break;  // the run ends in the item's fixed cost: the next CTA begins it
     const long long row0 = (long long)w.tile * ROWS;
 
     // ---- the query rows as fragments: register pairs (0, 4), (1, 5)/16, (2, 6), (3, 7)/16 of
     // each 8 channels, as the levels come out of a word
     uint32_t aq[PARTS][NG][2][4];
-    float qs[NT][NG], f[NT];
+    // sum(q_g) 2^-24 in three bf16 parts, against the lows of two groups a lane: with 4 groups
+    // k-pairs q = 0, 1 hold the first part of groups (0, 1) and (2, 3), 2 and 3 the second, 8 behind
+    // them the third; with 2 groups q = 0, 1, 2 hold the three parts
+    uint32_t al[4] = {0, 0, 0, 0};
+    float f[NT];
     int lim[NT];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -417,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       long long t;
       int h, i;
       const bool have = row_of(p, s, w.head, row0 + x * 8 + r, &t, &h, &i);
-      float v[NG][8];
+      float v[NG][8], qs[NG];
       float mx = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -454,7 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
         }
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        qs[x & (NT - 1)][g] = sum * 0x1p-24f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float sc = (j & 1) ? 0.0625f : 1.f;
@@ -467,6 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
                 pack_half2(lo - __low2float(back), hi - __high2float(back));
           }
         }
+        qs[g] = sum * 0x1p-24f;
+      }
+      if constexpr (NG == 4) {
+        float u = (q & 1) ? qs[2] : qs[0], w2 = (q & 1) ? qs[3] : qs[1];
+        const uint32_t p0 = take_bf16(u, w2), p1 = take_bf16(u, w2), p2 = take_bf16(u, w2);
+        al[x] = q < 2 ? p0 : p1;
+        al[2 + x] = q < 2 ? p2 : 0;
+      } else {
+        float u = qs[0], w2 = qs[1];
+        const uint32_t p0 = take_bf16(u, w2), p1 = take_bf16(u, w2), p2 = take_bf16(u, w2);
+        al[x] = q == 0 ? p0 : q == 1 ? p1 : q == 2 ? p2 : 0;
       }
     }
     int lim_min = lim[0], lim_max = lim[0] == INT_MAX ? 0 : lim[0];
@@ -477,14 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     lim_min = __reduce_min_sync(0xFFFFFFFFu, lim_min);
     lim_max = __reduce_max_sync(0xFFFFFFFFu, lim_max);
 
-    float o[NT][NG][2][4], om[NT][NG], l[NT], m[NT];
+    // outputs; and rows 0 to NG - 1 the lows' sums of the groups, row 4 the weights' sum
+    // rows' references: ms for the logits, me (an exponent as bf16 holds it) for the magnitude of the
+    // values, common to all rows; weights are 2^(logit - m), m = ms + (me - 127) - kHead
+    float o[NT][NG][2][4], ol[NT][4], m[NT], ms[NT];
+    uint32_t me = 0, big = 0;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      l[x] = 0.f;
-      m[x] = -FLT_MAX;
+      m[x] = ms[x] = -FLT_MAX;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ol[x][c] = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        om[x][g] = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -499,77 +577,102 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       const unsigned char* kp = base + page * (D / 2) + row * (D / 8);
       const unsigned char* vl = kl + rec;
       const unsigned char* vp = kp + rec;
-      // the exponent of the tile's largest scale or low
+      // each lane unpacks the scales of half a token (4 groups) or a whole one, for all lanes
+      // to read, and looks at the largest magnitude of its values' scales and lows
       uint32_t top = 0;
       {
         const Words<NG / 2> e = lds_words<NG / 2>(vp + lane * (D / 16));
+        const Words<NG / 2> k = lds_words<NG / 2>(kp + lane * (D / 16));
         const bool in = !kMask || pos + (lane >> 1) < lim_max;
 #pragma unroll
         for (int g = 0; g < NG / 2; ++g) {
-          const uint32_t lo = e.w[g] & 0x7FFFu, hi = (e.w[g] >> 16) & 0x7FFFu;
-          top = max(top, lo < 0x7F80u ? lo : 0u);
-          top = max(top, hi < 0x7F80u ? hi : 0u);
+          top = __vmaxu2(top, e.w[g] & 0x7FFF7FFFu);
+          ks[lane * (NG / 2) + g] = scale_of(k.w[g]);
+          vs[lane * (NG / 2) + g] = in ? scale_of(e.w[g]) : 0.f;
         }
         if (!in) top = 0;
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
       }
-      const float ex = fmaxf((float)((int)(top >> 7) - 127), -80.f);
-      // ---- logits
+      __syncwarp();
+      // ---- logits (without the row's factor f)
       float sv[NT][4];  // tokens a, b of the first 8, then of the second
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const Words<NG> wk = lds_words<NG>(kl + (hf * 8 + tok_k) * (D / 2) + q * (D / 8));
-        const Words<NG> pa = lds_words<NG>(kp + (hf * 8 + tok_a) * (D / 8));
-        const Words<NG> pb = lds_words<NG>(kp + (hf * 8 + tok_b) * (D / 8));
-        float t0[NT] = {}, t1[NT] = {};
+        const Words<2> pl = lds_words<2>(kp + (hf * 8 + tok_k) * (D / 8) + (NG == 4 ? (q & 1) * 8 : 0));
+        const Words<NG> sa = lds_words<NG>(ks + (hf * 8 + tok_a) * NG);
+        const Words<NG> sb = lds_words<NG>(ks + (hf * 8 + tok_b) * NG);
+        const uint32_t lows = __byte_perm(pl.w[0], pl.w[1], 0x7632);
+        float acc[4];
+        mma_bf16_first(acc, al, lows, lows);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          float d[4];
           const uint32_t x = wk.w[g], y = x >> 8;
-#pragma unroll
-          for (int pt = 0; pt < PARTS; ++pt) {
-            mma16816(d, aq[pt][g][0], x & 0x000F000Fu, x & 0x00F000F0u);
-            mma16816(d, aq[pt][g][1], y & 0x000F000Fu, y & 0x00F000F0u);
+          mma_f16_first(d, aq[0][g][0], x & 0x000F000Fu, x & 0x00F000F0u);
+          mma_f16(d, aq[0][g][1], y & 0x000F000Fu, y & 0x00F000F0u);
+          if constexpr (PARTS == 2) {
+            mma_f16(d, aq[PARTS - 1][g][0], x & 0x000F000Fu, x & 0x00F000F0u);
+            mma_f16(d, aq[PARTS - 1][g][1], y & 0x000F000Fu, y & 0x00F000F0u);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            t0[nt] = fmaf(scale_of(pa.w[g]), d[2 * nt], fmaf(low_of(pa.w[g]), qs[nt][g], t0[nt]));
-            t1[nt] = fmaf(scale_of(pb.w[g]), d[2 * nt + 1], fmaf(low_of(pb.w[g]), qs[nt][g], t1[nt]));
+            acc[2 * nt] = fmaf(__uint_as_float(sa.w[g]), d[2 * nt], acc[2 * nt]);
+            acc[2 * nt + 1] = fmaf(__uint_as_float(sb.w[g]), d[2 * nt + 1], acc[2 * nt + 1]);
           }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          sv[nt][2 * hf] = t0[nt] * f[nt];
-          sv[nt][2 * hf + 1] = t1[nt] * f[nt];
+          sv[nt][2 * hf] = acc[2 * nt];
+          sv[nt][2 * hf + 1] = acc[2 * nt + 1];
           if constexpr (kMask) {
             if (pos + hf * 8 + tok_a >= lim[nt]) sv[nt][2 * hf] = -INFINITY;
             if (pos + hf * 8 + tok_b >= lim[nt]) sv[nt][2 * hf + 1] = -INFINITY;
           }
         }
       }
-      // ---- the reference M, moved only when it has to
-      bool need = false;
+      // ---- the references, moved only when they have to
+      bool need = __vmaxu2(top, big) != big;
       float mx[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mx[nt] = fmaxf(fmaxf(sv[nt][0], sv[nt][1]), fmaxf(sv[nt][2], sv[nt][3])) + (ex - kHead);
-        need |= mx[nt] > m[nt] + kLazy;
+        mx[nt] = fmaxf(fmaxf(sv[nt][0], sv[nt][1]), fmaxf(sv[nt][2], sv[nt][3])) * f[nt];
+        need |= mx[nt] > ms[nt] + kLazy;
       }
       if (__any_sync(0xFFFFFFFFu, need)) {
+        uint32_t e = max((top & 0xFFFFu) < 0x7F80u ? top & 0xFFFFu : 0u,
+                         (top >> 16) < 0x7F80u ? top >> 16 : 0u);
+        if (top >= 0x7F800000u || (top & 0xFFFFu) >= 0x7F80u) {  // a NaN hides its lane's others
+          e = 0;
+          const Words<NG / 2> w2 = lds_words<NG / 2>(vp + lane * (D / 16));
+#pragma unroll
+          for (int g = 0; g < NG / 2; ++g) {
+            const uint32_t lo = w2.w[g] & 0x7FFFu, hi = (w2.w[g] >> 16) & 0x7FFFu;
+            e = max(e, lo < 0x7F80u ? lo : 0u);
+            e = max(e, hi < 0x7F80u ? hi : 0u);
+          }
+        }
+        e = max(__reduce_max_sync(0xFFFFFFFFu, e) >> 7, 47u);
+        const float de = e > me ? (float)((int)e - (int)me) : 0.f;
+        if (e > me) {
+          me = e;
+          const uint32_t lim16 = min(((e + (int)kLazy) << 7) | 0x7Fu, 0x7F7Fu);
+          big = lim16 | (lim16 << 16);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float mn = mx[nt];
           mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 1));
           mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2));
-          mn = fmaxf(mn, m[nt]);
-          const float alpha = exp2f(m[nt] - mn);
-          m[nt] = mn;
-          l[nt] *= alpha;
+          mn = fmaxf(mn, ms[nt]);
+          const float alpha = exp2f(ms[nt] - mn - de);
+          ms[nt] = mn;
+          m[nt] = mn + ((float)((int)me - 127) - kHead);
           const float a0 = __shfl_sync(0xFFFFFFFFu, alpha, 8 * q);
           const float a1 = __shfl_sync(0xFFFFFFFFu, alpha, 8 * q + 4);
+          ol[nt][0] *= a0;
+          ol[nt][1] *= a1;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            om[nt][g] *= alpha;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               o[nt][g][j][0] *= a0;
@@ -586,24 +689,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          pw[nt][c] = ex2_approx(sv[nt][c] - m[nt]);
-          l[nt] += pw[nt][c];
+          pw[nt][c] = ex2_approx(fmaf(sv[nt][c], f[nt], -m[nt]));
+          if constexpr (PARTS == 1)  // cut to tf32: one value for the sums and the products
+            pw[nt][c] = __uint_as_float(__float_as_uint(pw[nt][c]) & 0xFFFFE000u);
         }
-      // ---- values
-      const Words<NG / 2> va0 = lds_words<NG / 2>(vl + tok_a * (D / 2) + (r ^ (NG == 4 ? (q & 1) * 4 : 0)) * (D / 16));
-      const Words<NG / 2> vb0 = lds_words<NG / 2>(vl + tok_b * (D / 2) + (r ^ (NG == 4 ? (q & 1) * 4 : 0)) * (D / 16));
-      const Words<NG / 2> va1 = lds_words<NG / 2>(vl + (8 + tok_a) * (D / 2) + (r ^ (NG == 4 ? (q & 1) * 4 : 0)) * (D / 16));
-      const Words<NG / 2> vb1 = lds_words<NG / 2>(vl + (8 + tok_b) * (D / 2) + (r ^ (NG == 4 ? (q & 1) * 4 : 0)) * (D / 16));
-      const Words<NG> pr[4] = {lds_words<NG>(vp + tok_a * (D / 8)), lds_words<NG>(vp + tok_b * (D / 8)),
-                               lds_words<NG>(vp + (8 + tok_a) * (D / 8)), lds_words<NG>(vp + (8 + tok_b) * (D / 8))};
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float sc[4], lw[4];
+      // ---- lows of the values and the weights' sum: the lows as they are (row g of the first
+      // operand), ones (row 4), against the weights in tf32 (in two parts of fp32 rows)
+      {
+        const unsigned char* lp = vp + (r & (NG - 1)) * 4;
+        uint32_t lw[4] = {*reinterpret_cast<const uint32_t*>(lp + tok_a * (D / 8)),
+                          *reinterpret_cast<const uint32_t*>(lp + tok_b * (D / 8)),
+                          *reinterpret_cast<const uint32_t*>(lp + (8 + tok_a) * (D / 8)),
+                          *reinterpret_cast<const uint32_t*>(lp + (8 + tok_b) * (D / 8))};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          sc[c] = scale_of(pr[c].w[g]);
-          lw[c] = low_of(pr[c].w[g]);
+          lw[c] &= 0xFFFF0000u;
+          if constexpr (kMask) {
+            // nothing from behind the last token; a NaN reaches the rows that see it through its
+            // scale below, and must not meet the weight 0 of a row that does not
+            const bool in = pos + (c >> 1) * 8 + ((c & 1) ? tok_b : tok_a) < lim_max;
+            if (!in || (lw[c] & 0x7F800000u) == 0x7F800000u) lw[c] = 0;
+          }
+          if (r == 4) lw[c] = 0x3F800000u;
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t x[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = __float_as_uint(pw[nt][c]) & 0xFFFFE000u;
+          mma_tf32(ol[nt], lw[0], lw[1], x[0], x[1]);
+          mma_tf32(ol[nt], lw[2], lw[3], x[2], x[3]);
+          if constexpr (PARTS == 2) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[c] = __float_as_uint(pw[nt][c] - __uint_as_float(x[c]));
+            mma_tf32(ol[nt], lw[0], lw[1], x[0], x[1]);
+            mma_tf32(ol[nt], lw[2], lw[3], x[2], x[3]);
+          }
+        }
+      }
+      // ---- values
+      const unsigned char* vl2 = vl + (r ^ (NG == 4 ? (q & 1) * 4 : 0)) * (D / 16);
+      const Words<NG / 2> va0 = lds_words<NG / 2>(vl2 + tok_a * (D / 2));
+      const Words<NG / 2> vb0 = lds_words<NG / 2>(vl2 + tok_b * (D / 2));
+      const Words<NG / 2> va1 = lds_words<NG / 2>(vl2 + (8 + tok_a) * (D / 2));
+      const Words<NG / 2> vb1 = lds_words<NG / 2>(vl2 + (8 + tok_b) * (D / 2));
+      const Words<NG> sc[4] = {lds_words<NG>(vs + tok_a * NG), lds_words<NG>(vs + tok_b * NG),
+                               lds_words<NG>(vs + (8 + tok_a) * NG), lds_words<NG>(vs + (8 + tok_b) * NG)};
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
         const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
         const uint32_t x0 = __byte_perm(va0.w[g >> 1], vb0.w[g >> 1], sel), y0 = x0 >> 8;
         const uint32_t x1 = __byte_perm(va1.w[g >> 1], vb1.w[g >> 1], sel), y1 = x1 >> 8;
@@ -614,49 +747,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
           float pv[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            pv[c] = pw[nt][c] * sc[c];
-            float add = pw[nt][c] * lw[c];
-            if constexpr (kMask) {  // 0 * NaN in a hidden place
-              const bool hidden = pos + (c >> 1) * 8 + ((c & 1) ? tok_b : tok_a) >= lim[nt];
-              if (hidden || pos + (c >> 1) * 8 + ((c & 1) ? tok_b : tok_a) >= lim_max) pv[c] = add = 0.f;
-            }
-            om[nt][g] += add;
+            pv[c] = pw[nt][c] * __uint_as_float(sc[c].w[g]);
+            if constexpr (kMask)  // 0 * NaN in a hidden place
+              if (pos + (c >> 1) * 8 + ((c & 1) ? tok_b : tok_a) >= lim[nt]) pv[c] = 0.f;
           }
           const uint32_t b0 = pack_half2(pv[0], pv[1]), b1 = pack_half2(pv[2], pv[3]);
-          mma16816(o[nt][g][0], f0, b0, b1);
-          mma16816(o[nt][g][1], f1, b0, b1);
+          mma_f16(o[nt][g][0], f0, b0, b1);
+          mma_f16(o[nt][g][1], f1, b0, b1);
           if constexpr (PARTS == 2) {
             const __half2 h0 = *reinterpret_cast<const __half2*>(&b0);
             const __half2 h1 = *reinterpret_cast<const __half2*>(&b1);
             const uint32_t c0 = pack_half2(pv[0] - __low2float(h0), pv[1] - __high2float(h0));
             const uint32_t c1 = pack_half2(pv[2] - __low2float(h1), pv[3] - __high2float(h1));
-            mma16816(o[nt][g][0], f0, c0, c1);
-            mma16816(o[nt][g][1], f1, c0, c1);
+            mma_f16(o[nt][g][0], f0, c0, c1);
+            mma_f16(o[nt][g][1], f1, c0, c1);
           }
         }
       }
     };
 
-    const int my_page = warp * kTile / page, my_row = warp * kTile % page;
-    for (int u = begin; u < end; ++u, ++n) {
-      const int st = n % C::kStages;
-      if (ok) ok = mbar_wait_bounded(&full[st], (n / C::kStages) & 1, abort_flag, kTimeoutNs);
+    const int page_log = __ffs(page) - 1;
+    for (; (tile >> 3) - base_n < end - begin; tile += W) {
+      st += (tile >> 3) - stage;
+      stage = tile >> 3;
+      if (st >= C::kStages) {
+        st -= C::kStages;
+        phase ^= 1;
+      }
+      if (ok) ok = mbar_wait_bounded(&full[st], phase, abort_flag, kTimeoutNs);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok) {
-        const int pos = s_meta[st * 8 + my_page] + my_row;
-        const unsigned char* base = smem + st * C::kStageBytes + my_page * 2 * rec;
+        const int pg = (tile & 7) * kTile >> page_log, row = (tile & 7) * kTile & (page - 1);
+        const int pos = s_meta[st * 8 + pg] + row;
+        const unsigned char* base = smem + st * C::kStageBytes + pg * 2 * rec;
         if (pos + kTile <= lim_min)
-          step(base, my_row, pos, std::false_type{});
+          step(base, row, pos, std::false_type{});
         else if (pos < lim_max)
-          step(base, my_row, pos, std::true_type{});
+          step(base, row, pos, std::true_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
       }
     }
+    base_n += end - begin;
     if (!ok && lane == 0 && !*abort_flag) fail();
 
     // ---- join the 8 warps: each leaves its rows' outputs and sums in shared memory
-    consumers_sync();  // the previous item's have been read
+    consumers_sync<kWarps * 32>();  // the previous item's have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -668,20 +804,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
               make_float4(o[nt][g][0][c] * 0x1p24f, o[nt][g][0][2 + c] * 0x1p20f,
                           o[nt][g][1][c] * 0x1p24f, o[nt][g][1][2 + c] * 0x1p20f);
         }
-        om[nt][g] += __shfl_xor_sync(0xFFFFFFFFu, om[nt][g], 1);
-        om[nt][g] += __shfl_xor_sync(0xFFFFFFFFu, om[nt][g], 2);
       }
-      l[nt] += __shfl_xor_sync(0xFFFFFFFFu, l[nt], 1);
-      l[nt] += __shfl_xor_sync(0xFFFFFFFFu, l[nt], 2);
-      if (q == 0) {
-        float* st = s_stat + (warp * ROWS + nt * 8 + r) * C::kStat;
-        st[0] = m[nt];
-        st[1] = l[nt];
+      // lane (r, q) has row r of the sums for heads 2q and 2q + 1
 #pragma unroll
-        for (int g = 0; g < NG; ++g) st[2 + g] = om[nt][g];
+      for (int c = 0; c < 2; ++c) {
+        float* st = s_stat + (warp * ROWS + nt * 8 + 2 * q + c) * C::kStat;
+        if (r == 4) st[1] = ol[nt][c];
+        if (r < NG) st[2 + r] = ol[nt][c];
       }
+      if (q == 0) s_stat[(warp * ROWS + nt * 8 + r) * C::kStat] = m[nt];
     }
-    consumers_sync();
+    consumers_sync<kWarps * 32>();
     const bool whole = begin == 0 && end == w.units;
     const int slot = 2 * cta + (begin == 0 ? 1 : 0);
     constexpr int kPerRow = D / 4;  // threads of a row, 4 channels each
@@ -722,12 +855,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     }
     if (!whole && begin == 0 && threadIdx.x == 0) {
       // the item goes on in the CTAs up to the one that owns its last unit
-      const long long last = u1 - w.left + w.units - 1;
+      const long long last = u1 - w.left + units_cost(w.units) - 1;
       const int owner = (int)(((last + 1) * ctas + total - 1) / total) - 1;
       p.parts[cta] = Part{owner - cta + 1, w.b, w.head, w.tile};
     }
-    w.left -= end - begin;
-    if (w.left > 0) next_item<ROWS>(p, w);
+    next_item<ROWS>(p, w);
   }
 }
 
@@ -764,16 +896,16 @@ __global__ void __launch_bounds__(D) kv4_join_kernel(const __grid_constant__ Par
     *dst = __float2bfloat16(acc * inv);
 }
 
-template <int D, int NT, typename T>
+template <int D, int NT, int W, typename T>
 int launch(const Params& p, cudaStream_t stream) {
-  using C = Cfg<D, NT>;
-  auto kern = kv4_attend_kernel<D, NT, T>;
+  using C = Cfg<D, NT, W>;
+  auto kern = kv4_attend_kernel<D, NT, W, T>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return SBSA_ERR_CUDA;
   int grid = sm_count();
   if (grid <= 0) return SBSA_ERR_CUDA;
   grid = grid < kMaxCtas ? grid : kMaxCtas;
-  kern<<<grid, kThreads, C::kSmem, stream>>>(p);
+  kern<<<grid, C::kThreads, C::kSmem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SBSA_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -805,10 +937,10 @@ int launch_kv4_attend(const Kv4AttendArgs& a, cudaStream_t stream) {
   // 16 rows share a read of the cache where a sequence has more than 8
   const bool two = (long long)p.group * a.max_new > 8;
   if (a.dtype == SBSA_FP32)
-    return a.d == 64 ? launch<64, 1, float>(p, stream) : launch<128, 1, float>(p, stream);
+    return a.d == 64 ? launch<64, 1, 8, float>(p, stream) : launch<128, 1, 8, float>(p, stream);
   if (a.d == 64)
-    return two ? launch<64, 2, __nv_bfloat16>(p, stream) : launch<64, 1, __nv_bfloat16>(p, stream);
-  return two ? launch<128, 2, __nv_bfloat16>(p, stream) : launch<128, 1, __nv_bfloat16>(p, stream);
+    return two ? launch<64, 2, 8, __nv_bfloat16>(p, stream) : launch<64, 1, 12, __nv_bfloat16>(p, stream);
+  return two ? launch<128, 2, 8, __nv_bfloat16>(p, stream) : launch<128, 1, 12, __nv_bfloat16>(p, stream);
 }
 
 }  // namespace sbsa
