@@ -14,11 +14,11 @@
 // 110 cycles for 16 tokens (d = 128, 2560 bytes), and the work on them is
 // about 280 warp instructions (70 issue cycles) at 8 rows: levels must be
 // unpacked with next to nothing, which rules out a copy in fp16 through shared
-// memory for tcgen05 (its writes and reads alone would exceed the shared
-// memory's bandwidth).  The products therefore run on mma.sync m16n8k16, whose
-// operands are registers: S = Q K^T with the rows as M (8 or 16 query rows) and
-// 8 tokens as N, so that a lane's logits are in the place where P^T is the second
-// operand of O^T = V^T P^T with 16 channels as M.
+// memory for tcgen05 (its writes and reads alone would exceed the shared memory's
+// bandwidth).  The products therefore run on mma.sync m16n8k16, whose
+// operands are registers: S^T = K Q^T with 16 tokens as M and 8 query rows as N, and
+// O^T = V^T P^T with 16 channels as M; in between the scaled weights are transposed
+// (movmatrix), so that a lane holds scales and lows of two tokens, not four.
 //
 // The rows of one kv head (or listed query head) of a sequence, in tiles of
 // kRows, are an item; an item's tokens fall into units of 128 (one stage).  The
@@ -44,26 +44,27 @@ namespace sbsa {
 namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kTile = 16;         // tokens of a warp's step
-constexpr int kUnit = 8 * kTile;  // tokens of a stage: 8 warps take it
+constexpr int kUnit = 128;  // tokens of a stage
 constexpr int kMaxCtas = 160;
 // Weights are 2^(S - M), M = (reference of the logits) + (reference of the
 // values' exponents) - kHead; each reference moves only when it is outgrown by more
 // than kLazy, so the fp16 weights times a scale stay below 2^(kHead + 2 kLazy + 1) = 2^15.
 constexpr float kHead = 6.f, kLazy = 4.f;
 
-// W computing warps take the tiles of 16 tokens in turn.  8 bf16 rows leave
-// registers for 12; 16 rows or two-part fp32 rows take 8 (spilled registers cost
-// far more than warps gain: next to the ring the L1 has a few KB left).  The copying
-// warp and its three idle neighbours are a warpgroup whose registers the computing
-// warps take over.
-template <int D, int NT, int W>
+// 8 computing warps take the tiles of 16 TT tokens in turn; with two of them a
+// scheduler the latency of a tile's chain (levels, products, weights, products) is what
+// they wait for, so 8 rows take two tiles of 16 at once.  The copying warp and its
+// three idle neighbours are a warpgroup whose registers the computing warps take
+// over: 256 * 224 + 128 * 56 = 384 * 168, what the block is launched with.
+constexpr int kWarps = 8;
+constexpr int kThreads = (kWarps + 4) * 32;
+constexpr int kRegs = 224, kRegsCopy = 56;
+
+template <int D, int NT>
 struct Cfg {
-  static constexpr int kWarps = W;
-  static constexpr int kThreads = (W + 4) * 32;
-  // launched with 128 (512 threads) or 168 (384) registers a thread: 384 * 152 + 128 * 56 =
-  // 512 * 128, 256 * 224 + 128 * 56 = 384 * 168
-  static constexpr int kRegs = W == 12 ? 152 : 224, kRegsCopy = 56;
+  static constexpr int kSub = NT == 1 ? 2 : 1;    // TT
+  static constexpr int kTile = 16 * kSub;         // tokens of a warp's step
+  static constexpr int kTiles = kUnit / kTile;    // of a stage
   static constexpr int kRows = 8 * NT;
   static constexpr int kGroups = D / 32;
   static constexpr int kStageBytes = kUnit * (D / 8) * 10;
@@ -73,14 +74,12 @@ struct Cfg {
   static constexpr int kOffStat = kOffOut + kWarps * kRows * kOutStride * 4;
   // per warp and row: M, l, and the lows' sums of the groups
   static constexpr int kStat = 2 + kGroups;
-  // per warp: its tokens' key and value scales in fp32
-  static constexpr int kOffScale = kOffStat + kWarps * kRows * kStat * 4;
-  static constexpr int kOffMeta = kOffScale + kWarps * 2 * kTile * kGroups * 4;
+  static constexpr int kOffMeta = kOffStat + kWarps * kRows * kStat * 4;
   static constexpr int kOffScan = kOffMeta + kStages * 8 * 4;
   static constexpr int kOffBar = kOffScan + (kThreads / 32 + 1) * 8 + 32;
   static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(kOffBar % 8 == 0 && kOffScan % 8 == 0 && kOffScale % 16 == 0, "alignment");
+  static_assert(kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
 };
 
 struct Part {  // which item's first part a CTA holds, in how many parts (0: none)
@@ -190,13 +189,11 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// D += A B on tf32, 16 x 8 by 8 x 8; rows 8 to 15 of A are zero.
-__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(0), "r"(a2), "r"(b0), "r"(b1));
+// Transpose of an 8 x 8 matrix of 16-bit elements (row lane / 4, columns 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Two fp32 values as their bf16 parts: returns the leading parts and leaves the rest.
@@ -214,6 +211,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 __device__ __forceinline__ float scale_of(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float low_of(uint32_t pair) {
+  return __uint_as_float(pair & 0xFFFF0000u);
+}
 // The words of one token's chunk of levels, or its pairs, for all groups.
 template <int NG>
 struct Words {
@@ -233,6 +233,13 @@ __device__ __forceinline__ Words<NG> lds_words(const void* p) {
   }
   return r;
 }
+
+// Tiles of 16 tokens: the page's keys, the tile's first token there, its position.
+template <int TT>
+struct Tiles {
+  const unsigned char* base[TT];
+  int row[TT], pos[TT];
+};
 
 // 8 channels of a query row, as fp32.
 __device__ __forceinline__ void load_q8(const __nv_bfloat16* p, float (&x)[8]) {
@@ -274,14 +281,13 @@ __device__ __forceinline__ void consumers_sync() {
 // bits), and so do their weights; a bf16 row is one fp16 part exactly (its
 // elements are scaled by a power of two so that the largest is near 2^10) and
 // the weights are rounded to fp16 once, 2^-11 of each.
-template <int D, int NT, int W, typename T>
-__global__ void __launch_bounds__((W + 4) * 32, 1)
-    kv4_attend_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<D, NT, W>;
-  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
+template <int D, int NT, typename T>
+__global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, NT>;
   constexpr int NG = C::kGroups;
   constexpr int ROWS = C::kRows;
   constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
+  constexpr int TT = C::kSub;
   extern __shared__ __align__(128) unsigned char smem[];
   float* s_out = reinterpret_cast<float*>(smem + C::kOffOut);
   float* s_stat = reinterpret_cast<float*>(smem + C::kOffStat);
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 8);
+      mbar_init(&empty[s], C::kTiles);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -353,15 +359,13 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
   w.left = w.cost + u1 - u0;
   item_size<ROWS>(p, w.b, w.head, &w.units, &w.tiles);
 
-  float* ks = reinterpret_cast<float*>(smem + C::kOffScale) + warp * 2 * kTile * NG;
-  float* vs = ks + kTile * NG;
   auto fail = [&]() {
     *abort_flag = 1;
     if (p.a.b.status) atomicCAS(p.a.b.status, 0, SBSA_ERR_TIMEOUT);
   };
 
   if (warp >= kWarps) {
-    regs_lower<C::kRegsCopy>();
+    regs_lower<kRegsCopy>();
     if (warp > kWarps) return;
     // ================================================================ copies
     const int pages = kUnit / page;
@@ -442,16 +446,17 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
   }
 
   // ==================================================================== products
-  regs_raise<C::kRegs>();
+  regs_raise<kRegs>();
   const int r = lane >> 2, q = lane & 3;
-  // Column n of S is token n ^ (n >> 2) of 8: with it neither the keys', the
-  // values' nor the pairs' reads meet a bank twice.  A lane's logits are those of
-  // columns 2q and 2q + 1, its key rows' that of column r.
-  const int tok_k = r ^ (r >> 2);
+  // Row r of the first product is token r ^ (r >> 2) of 8: with it neither the keys' nor the values'
+  // reads meet a bank twice.  A lane has the keys and weights of tokens tok and tok + 8 of a tile, and
+  // the values of the tokens of rows 2q and 2q + 1.
+  const int tok = r ^ (r >> 2);
   const int tok_a = (2 * q) ^ (q >> 1), tok_b = (2 * q + 1) ^ (q >> 1);
-  // this warp's next tile (8 to a stage), and its stage's number and place in the ring
+  // this warp's next tile, and its stage's number and place in the ring
   int tile = warp, stage = 0, st = 0, phase = 0;
   int base_n = 0;                    // the number of the item's first stage
+  const int page_log = __ffs(page) - 1;
   bool ok = true;
   while (w.left > 0) {
     const Seq s = seq_of(p, w.b);
@@ -459,25 +464,19 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
     if (begin >= end) break;  // the run ends in the item's fixed cost: the next CTA begins it
     const long long row0 = (long long)w.tile * ROWS;
 
-    // ---- the query rows as fragments: register pairs (0, 4), (1, 5)/16, (2, 6), (3, 7)/16 of
-    // each 8 channels, as the levels come out of a word
-    uint32_t aq[PARTS][NG][2][4];
+    // ---- the query rows as fragments: elements (0, 4), (1, 5)/16, (2, 6), (3, 7)/16 of each 8
+    // channels, as the levels come out of a word
+    uint32_t bq[NT][PARTS][NG][2][2];
     // sum(q_g) 2^-24 in three bf16 parts, against the lows of two groups a lane: with 4 groups
     // k-pairs q = 0, 1 hold the first part of groups (0, 1) and (2, 3), 2 and 3 the second, 8 behind
     // them the third; with 2 groups q = 0, 1, 2 hold the three parts
-    uint32_t al[4] = {0, 0, 0, 0};
-    float f[NT];
-    int lim[NT];
+    uint32_t bl[NT][2];
+    // of rows 2q and 2q + 1: the factor of the logits, and the first token that is not seen
+    float f[NT][2];
+    int lim[NT][2];
+    int lim_min = INT_MAX, lim_max = 0;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (x >= NT) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int pt = 0; pt < PARTS; ++pt)
-            aq[pt][g][0][1] = aq[pt][g][0][3] = aq[pt][g][1][1] = aq[pt][g][1][3] = 0;
-        continue;
-      }
+    for (int x = 0; x < NT; ++x) {
       long long t;
       int h, i;
       const bool have = row_of(p, s, w.head, row0 + x * 8 + r, &t, &h, &i);
@@ -499,14 +498,21 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
       const int e = clamp_int(137 - (int)(__float_as_uint(mx) >> 23), -90, 100);
       const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-      f[x & (NT - 1)] = p.scale_log2 * __uint_as_float((uint32_t)(24 - e + 127) << 23);
+      const float fr = p.scale_log2 * __uint_as_float((uint32_t)(24 - e + 127) << 23);
       // rows that see nothing (before the sequence, beyond max_new) mask all; rows past the
       // tile's last mask nothing, so that they never send the warp to the masked path
-      lim[x & (NT - 1)] = INT_MAX;
+      int lr = INT_MAX;
       if (have) {
         const int visible = s.len - s.rows + i + 1;
-        lim[x & (NT - 1)] = i < p.a.max_new ? max(visible, 0) : 0;
+        lr = i < p.a.max_new ? max(visible, 0) : 0;
         if ((visible < 1 || i >= p.a.max_new) && q == 0) kv4_record(p.a.b.status);
+        lim_min = min(lim_min, lr);
+        lim_max = max(lim_max, lr);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        f[x][c] = __shfl_sync(0xFFFFFFFFu, fr, 8 * q + 4 * c);
+        lim[x][c] = __shfl_sync(0xFFFFFFFFu, lr, 8 * q + 4 * c);
       }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -518,51 +524,55 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
         }
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        qs[g] = sum * 0x1p-24f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float sc = (j & 1) ? 0.0625f : 1.f;
           const float lo = v[g][j] * sc, hi = v[g][j + 4] * sc;
           const uint32_t h0 = pack_half2(lo, hi);
-          aq[0][g][j >> 1][(j & 1) * 2 + x] = h0;
+          bq[x][0][g][j >> 1][j & 1] = h0;
           if constexpr (PARTS == 2) {
             const __half2 back = *reinterpret_cast<const __half2*>(&h0);
-            aq[PARTS - 1][g][j >> 1][(j & 1) * 2 + x] =
+            bq[x][PARTS - 1][g][j >> 1][j & 1] =
                 pack_half2(lo - __low2float(back), hi - __high2float(back));
           }
         }
-        qs[g] = sum * 0x1p-24f;
       }
       if constexpr (NG == 4) {
         float u = (q & 1) ? qs[2] : qs[0], w2 = (q & 1) ? qs[3] : qs[1];
         const uint32_t p0 = take_bf16(u, w2), p1 = take_bf16(u, w2), p2 = take_bf16(u, w2);
-        al[x] = q < 2 ? p0 : p1;
-        al[2 + x] = q < 2 ? p2 : 0;
+        bl[x][0] = q < 2 ? p0 : p1;
+        bl[x][1] = q < 2 ? p2 : 0;
       } else {
         float u = qs[0], w2 = qs[1];
         const uint32_t p0 = take_bf16(u, w2), p1 = take_bf16(u, w2), p2 = take_bf16(u, w2);
-        al[x] = q == 0 ? p0 : q == 1 ? p1 : q == 2 ? p2 : 0;
+        bl[x][0] = q == 0 ? p0 : q == 1 ? p1 : q == 2 ? p2 : 0;
+        bl[x][1] = 0;
       }
-    }
-    int lim_min = lim[0], lim_max = lim[0] == INT_MAX ? 0 : lim[0];
-    if constexpr (NT == 2) {
-      lim_min = min(lim_min, lim[NT - 1]);
-      lim_max = max(lim_max, lim[NT - 1] == INT_MAX ? 0 : lim[NT - 1]);
     }
     lim_min = __reduce_min_sync(0xFFFFFFFFu, lim_min);
     lim_max = __reduce_max_sync(0xFFFFFFFFu, lim_max);
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (lim[x][c] == INT_MAX) lim[x][c] = lim_max;
 
-    // outputs; and rows 0 to NG - 1 the lows' sums of the groups, row 4 the weights' sum
     // rows' references: ms for the logits, me (an exponent as bf16 holds it) for the magnitude of the
-    // values, common to all rows; weights are 2^(logit - m), m = ms + (me - 127) - kHead
-    float o[NT][NG][2][4], ol[NT][4], m[NT], ms[NT];
+    // values, common to all rows; weights are 2^(logit - m), m = ms + (me - 127) - kHead.
+    // o: outputs; ol: the lows' sums of this lane's tokens, l: their weights' sums
+    float o[NT][NG][2][4], ol[NT][NG][2], l[NT][2], m[NT][2], ms[NT][2];
     uint32_t me = 0, big = 0;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      m[x] = ms[x] = -FLT_MAX;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) ol[x][c] = 0.f;
+      for (int c = 0; c < 2; ++c) {
+        m[x][c] = ms[x][c] = -FLT_MAX;
+        l[x][c] = 0.f;
+      }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        ol[x][g][0] = ol[x][g][1] = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -570,82 +580,92 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
       }
     }
 
-    // ---- one step: 16 tokens.  kMask: some row does not see all of them.
-    auto step = [&](const unsigned char* base, int row, int pos, auto mask_tag) {
+    // ---- one step: TT tiles of 16 tokens; base and row: the page's keys and the tile's first
+    // token there.  kMask: some row does not see all of them.
+    auto step = [&](const Tiles<TT>& at, auto mask_tag) {
       constexpr bool kMask = decltype(mask_tag)::value;
-      const unsigned char* kl = base + row * (D / 2);
-      const unsigned char* kp = base + page * (D / 2) + row * (D / 8);
-      const unsigned char* vl = kl + rec;
-      const unsigned char* vp = kp + rec;
-      // each lane unpacks the scales of half a token (4 groups) or a whole one, for all lanes
-      // to read, and looks at the largest magnitude of its values' scales and lows
-      uint32_t top = 0;
-      {
+      uint32_t top = 0;  // the largest magnitude of a scale or low that this lane looks at
+      float sv[TT][NT][4];  // logits (without f): token tok for rows 2q, 2q + 1, then token tok + 8
+      Words<NG> pv[TT][2];
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        const unsigned char* kl = at.base[tt] + at.row[tt] * (D / 2);
+        const unsigned char* kp = at.base[tt] + page * (D / 2) + at.row[tt] * (D / 8);
+        const unsigned char* vp = kp + rec;
+        const Words<NG> w0 = lds_words<NG>(kl + tok * (D / 2) + q * (D / 8));
+        const Words<NG> w1 = lds_words<NG>(kl + (8 + tok) * (D / 2) + q * (D / 8));
+        const Words<NG> p0 = lds_words<NG>(kp + tok * (D / 8));
+        const Words<NG> p1 = lds_words<NG>(kp + (8 + tok) * (D / 8));
+        pv[tt][0] = lds_words<NG>(vp + tok * (D / 8));
+        pv[tt][1] = lds_words<NG>(vp + (8 + tok) * (D / 8));
         const Words<NG / 2> e = lds_words<NG / 2>(vp + lane * (D / 16));
-        const Words<NG / 2> k = lds_words<NG / 2>(kp + lane * (D / 16));
-        const bool in = !kMask || pos + (lane >> 1) < lim_max;
+        const bool in = !kMask || at.pos[tt] + (lane >> 1) < lim_max;
 #pragma unroll
-        for (int g = 0; g < NG / 2; ++g) {
-          top = __vmaxu2(top, e.w[g] & 0x7FFF7FFFu);
-          ks[lane * (NG / 2) + g] = scale_of(k.w[g]);
-          vs[lane * (NG / 2) + g] = in ? scale_of(e.w[g]) : 0.f;
+        for (int g = 0; g < NG / 2; ++g)
+          if (in) top = __vmaxu2(top, e.w[g] & 0x7FFF7FFFu);
+        uint32_t a[4];
+        a[0] = __byte_perm(p0.w[0], p0.w[1], 0x7632);
+        a[1] = __byte_perm(p1.w[0], p1.w[1], 0x7632);
+        if constexpr (NG == 4) {
+          if (q & 1) {
+            a[0] = __byte_perm(p0.w[NG - 2], p0.w[NG - 1], 0x7632);
+            a[1] = __byte_perm(p1.w[NG - 2], p1.w[NG - 1], 0x7632);
+          }
         }
-        if (!in) top = 0;
-      }
-      __syncwarp();
-      // ---- logits (without the row's factor f)
-      float sv[NT][4];  // tokens a, b of the first 8, then of the second
+        a[2] = a[0];
+        a[3] = a[1];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const Words<NG> wk = lds_words<NG>(kl + (hf * 8 + tok_k) * (D / 2) + q * (D / 8));
-        const Words<2> pl = lds_words<2>(kp + (hf * 8 + tok_k) * (D / 8) + (NG == 4 ? (q & 1) * 8 : 0));
-        const Words<NG> sa = lds_words<NG>(ks + (hf * 8 + tok_a) * NG);
-        const Words<NG> sb = lds_words<NG>(ks + (hf * 8 + tok_b) * NG);
-        const uint32_t lows = __byte_perm(pl.w[0], pl.w[1], 0x7632);
-        float acc[4];
-        mma_bf16_first(acc, al, lows, lows);
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_first(sv[tt][nt], a, bl[nt][0], bl[nt][1]);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float d[4];
-          const uint32_t x = wk.w[g], y = x >> 8;
-          mma_f16_first(d, aq[0][g][0], x & 0x000F000Fu, x & 0x00F000F0u);
-          mma_f16(d, aq[0][g][1], y & 0x000F000Fu, y & 0x00F000F0u);
-          if constexpr (PARTS == 2) {
-            mma_f16(d, aq[PARTS - 1][g][0], x & 0x000F000Fu, x & 0x00F000F0u);
-            mma_f16(d, aq[PARTS - 1][g][1], y & 0x000F000Fu, y & 0x00F000F0u);
-          }
+          const uint32_t x0 = w0.w[g], x1 = w1.w[g], y0 = x0 >> 8, y1 = x1 >> 8;
+          const uint32_t f0[4] = {x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u};
+          const uint32_t f1[4] = {y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u};
+          const float s0 = scale_of(p0.w[g]), s1 = scale_of(p1.w[g]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            acc[2 * nt] = fmaf(__uint_as_float(sa.w[g]), d[2 * nt], acc[2 * nt]);
-            acc[2 * nt + 1] = fmaf(__uint_as_float(sb.w[g]), d[2 * nt + 1], acc[2 * nt + 1]);
+            float d[4];
+            mma_f16_first(d, f0, bq[nt][0][g][0][0], bq[nt][0][g][0][1]);
+            mma_f16(d, f1, bq[nt][0][g][1][0], bq[nt][0][g][1][1]);
+            if constexpr (PARTS == 2) {
+              mma_f16(d, f0, bq[nt][PARTS - 1][g][0][0], bq[nt][PARTS - 1][g][0][1]);
+              mma_f16(d, f1, bq[nt][PARTS - 1][g][1][0], bq[nt][PARTS - 1][g][1][1]);
+            }
+            sv[tt][nt][0] = fmaf(s0, d[0], sv[tt][nt][0]);
+            sv[tt][nt][1] = fmaf(s0, d[1], sv[tt][nt][1]);
+            sv[tt][nt][2] = fmaf(s1, d[2], sv[tt][nt][2]);
+            sv[tt][nt][3] = fmaf(s1, d[3], sv[tt][nt][3]);
           }
         }
+        if constexpr (kMask) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          sv[nt][2 * hf] = acc[2 * nt];
-          sv[nt][2 * hf + 1] = acc[2 * nt + 1];
-          if constexpr (kMask) {
-            if (pos + hf * 8 + tok_a >= lim[nt]) sv[nt][2 * hf] = -INFINITY;
-            if (pos + hf * 8 + tok_b >= lim[nt]) sv[nt][2 * hf + 1] = -INFINITY;
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (at.pos[tt] + tok + (c >> 1) * 8 >= lim[nt][c & 1]) sv[tt][nt][c] = -INFINITY;
         }
       }
       // ---- the references, moved only when they have to
       bool need = __vmaxu2(top, big) != big;
-      float mx[NT];
+      float mx[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mx[nt] = fmaxf(fmaxf(sv[nt][0], sv[nt][1]), fmaxf(sv[nt][2], sv[nt][3])) * f[nt];
-        need |= mx[nt] > ms[nt] + kLazy;
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = fmaxf(sv[0][nt][c], sv[0][nt][2 + c]);
+          if constexpr (TT == 2) x = fmaxf(x, fmaxf(sv[TT - 1][nt][c], sv[TT - 1][nt][2 + c]));
+          mx[nt][c] = x * f[nt][c];
+          need |= mx[nt][c] > ms[nt][c] + kLazy;
+        }
       if (__any_sync(0xFFFFFFFFu, need)) {
-        uint32_t e = max((top & 0xFFFFu) < 0x7F80u ? top & 0xFFFFu : 0u,
-                         (top >> 16) < 0x7F80u ? top >> 16 : 0u);
-        if (top >= 0x7F800000u || (top & 0xFFFFu) >= 0x7F80u) {  // a NaN hides its lane's others
-          e = 0;
-          const Words<NG / 2> w2 = lds_words<NG / 2>(vp + lane * (D / 16));
+        uint32_t e = 0;
 #pragma unroll
-          for (int g = 0; g < NG / 2; ++g) {
+        for (int tt = 0; tt < TT; ++tt) {
+          const Words<NG / 2> w2 =
+              lds_words<NG / 2>(at.base[tt] + rec + page * (D / 2) + at.row[tt] * (D / 8) + lane * (D / 16));
+          if (kMask && at.pos[tt] + (lane >> 1) >= lim_max) continue;
+#pragma unroll
+          for (int g = 0; g < NG / 2; ++g) {  // NaN groups say nothing
             const uint32_t lo = w2.w[g] & 0x7FFFu, hi = (w2.w[g] >> 16) & 0x7FFFu;
             e = max(e, lo < 0x7F80u ? lo : 0u);
             e = max(e, hi < 0x7F80u ? hi : 0u);
@@ -659,117 +679,89 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
           big = lim16 | (lim16 << 16);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float mn = mx[nt];
-          mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 1));
-          mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2));
-          mn = fmaxf(mn, ms[nt]);
-          const float alpha = exp2f(ms[nt] - mn - de);
-          ms[nt] = mn;
-          m[nt] = mn + ((float)((int)me - 127) - kHead);
-          const float a0 = __shfl_sync(0xFFFFFFFFu, alpha, 8 * q);
-          const float a1 = __shfl_sync(0xFFFFFFFFu, alpha, 8 * q + 4);
-          ol[nt][0] *= a0;
-          ol[nt][1] *= a1;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
+          for (int c = 0; c < 2; ++c) {
+            float mn = mx[nt][c];
+            mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 4));
+            mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 8));
+            mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 16));
+            mn = fmaxf(mn, ms[nt][c]);
+            const float alpha = exp2f(ms[nt][c] - mn - de);
+            ms[nt][c] = mn;
+            m[nt][c] = mn + ((float)((int)me - 127) - kHead);
+            l[nt][c] *= alpha;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              o[nt][g][j][0] *= a0;
-              o[nt][g][j][1] *= a1;
-              o[nt][g][j][2] *= a0;
-              o[nt][g][j][3] *= a1;
+            for (int g = 0; g < NG; ++g) {
+              ol[nt][g][c] *= alpha;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                o[nt][g][j][c] *= alpha;
+                o[nt][g][j][2 + c] *= alpha;
+              }
             }
           }
-        }
       }
-      // ---- weights
-      float pw[NT][4];
+      // ---- weights and values
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int tt = 0; tt < TT; ++tt) {
+        const unsigned char* vl =
+            at.base[tt] + rec + at.row[tt] * (D / 2) + (r ^ (NG == 4 ? (q & 1) * 4 : 0)) * (D / 16);
+        const Words<NG / 2> va0 = lds_words<NG / 2>(vl + tok_a * (D / 2));
+        const Words<NG / 2> vb0 = lds_words<NG / 2>(vl + tok_b * (D / 2));
+        const Words<NG / 2> va1 = lds_words<NG / 2>(vl + (8 + tok_a) * (D / 2));
+        const Words<NG / 2> vb1 = lds_words<NG / 2>(vl + (8 + tok_b) * (D / 2));
+        float pw[NT][4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          pw[nt][c] = ex2_approx(fmaf(sv[nt][c], f[nt], -m[nt]));
-          if constexpr (PARTS == 1)  // cut to tf32: one value for the sums and the products
-            pw[nt][c] = __uint_as_float(__float_as_uint(pw[nt][c]) & 0xFFFFE000u);
-        }
-      // ---- lows of the values and the weights' sum: the lows as they are (row g of the first
-      // operand), ones (row 4), against the weights in tf32 (in two parts of fp32 rows)
-      {
-        const unsigned char* lp = vp + (r & (NG - 1)) * 4;
-        uint32_t lw[4] = {*reinterpret_cast<const uint32_t*>(lp + tok_a * (D / 8)),
-                          *reinterpret_cast<const uint32_t*>(lp + tok_b * (D / 8)),
-                          *reinterpret_cast<const uint32_t*>(lp + (8 + tok_a) * (D / 8)),
-                          *reinterpret_cast<const uint32_t*>(lp + (8 + tok_b) * (D / 8))};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          lw[c] &= 0xFFFF0000u;
-          if constexpr (kMask) {
-            // nothing from behind the last token; a NaN reaches the rows that see it through its
-            // scale below, and must not meet the weight 0 of a row that does not
-            const bool in = pos + (c >> 1) * 8 + ((c & 1) ? tok_b : tok_a) < lim_max;
-            if (!in || (lw[c] & 0x7F800000u) == 0x7F800000u) lw[c] = 0;
-          }
-          if (r == 4) lw[c] = 0x3F800000u;
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint32_t x[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = __float_as_uint(pw[nt][c]) & 0xFFFFE000u;
-          mma_tf32(ol[nt], lw[0], lw[1], x[0], x[1]);
-          mma_tf32(ol[nt], lw[2], lw[3], x[2], x[3]);
-          if constexpr (PARTS == 2) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[c] = __float_as_uint(pw[nt][c] - __uint_as_float(x[c]));
-            mma_tf32(ol[nt], lw[0], lw[1], x[0], x[1]);
-            mma_tf32(ol[nt], lw[2], lw[3], x[2], x[3]);
-          }
-        }
-      }
-      // ---- values
-      const unsigned char* vl2 = vl + (r ^ (NG == 4 ? (q & 1) * 4 : 0)) * (D / 16);
-      const Words<NG / 2> va0 = lds_words<NG / 2>(vl2 + tok_a * (D / 2));
-      const Words<NG / 2> vb0 = lds_words<NG / 2>(vl2 + tok_b * (D / 2));
-      const Words<NG / 2> va1 = lds_words<NG / 2>(vl2 + (8 + tok_a) * (D / 2));
-      const Words<NG / 2> vb1 = lds_words<NG / 2>(vl2 + (8 + tok_b) * (D / 2));
-      const Words<NG> sc[4] = {lds_words<NG>(vs + tok_a * NG), lds_words<NG>(vs + tok_b * NG),
-                               lds_words<NG>(vs + (8 + tok_a) * NG), lds_words<NG>(vs + (8 + tok_b) * NG)};
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-        const uint32_t x0 = __byte_perm(va0.w[g >> 1], vb0.w[g >> 1], sel), y0 = x0 >> 8;
-        const uint32_t x1 = __byte_perm(va1.w[g >> 1], vb1.w[g >> 1], sel), y1 = x1 >> 8;
-        const uint32_t f0[4] = {x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u};
-        const uint32_t f1[4] = {y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu, y1 & 0x00F000F0u};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float pv[4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            pv[c] = pw[nt][c] * __uint_as_float(sc[c].w[g]);
-            if constexpr (kMask)  // 0 * NaN in a hidden place
-              if (pos + (c >> 1) * 8 + ((c & 1) ? tok_b : tok_a) >= lim[nt]) pv[c] = 0.f;
+            pw[nt][c] = ex2_approx(fmaf(sv[tt][nt][c], f[nt][c & 1], -m[nt][c & 1]));
+            l[nt][c & 1] += pw[nt][c];
           }
-          const uint32_t b0 = pack_half2(pv[0], pv[1]), b1 = pack_half2(pv[2], pv[3]);
-          mma_f16(o[nt][g][0], f0, b0, b1);
-          mma_f16(o[nt][g][1], f1, b0, b1);
-          if constexpr (PARTS == 2) {
-            const __half2 h0 = *reinterpret_cast<const __half2*>(&b0);
-            const __half2 h1 = *reinterpret_cast<const __half2*>(&b1);
-            const uint32_t c0 = pack_half2(pv[0] - __low2float(h0), pv[1] - __high2float(h0));
-            const uint32_t c1 = pack_half2(pv[2] - __low2float(h1), pv[3] - __high2float(h1));
-            mma_f16(o[nt][g][0], f0, c0, c1);
-            mma_f16(o[nt][g][1], f1, c0, c1);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+          const uint32_t x0 = __byte_perm(va0.w[g >> 1], vb0.w[g >> 1], sel), y0 = x0 >> 8;
+          const uint32_t x1 = __byte_perm(va1.w[g >> 1], vb1.w[g >> 1], sel), y1 = x1 >> 8;
+          const uint32_t f0[4] = {x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u};
+          const uint32_t f1[4] = {y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu, y1 & 0x00F000F0u};
+          const float sc[2] = {scale_of(pv[tt][0].w[g]), scale_of(pv[tt][1].w[g])};
+          const float lw[2] = {low_of(pv[tt][0].w[g]), low_of(pv[tt][1].w[g])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float x[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              x[c] = pw[nt][c] * sc[c >> 1];
+              if constexpr (kMask) {  // 0 * NaN in a hidden place
+                const bool hidden = at.pos[tt] + tok + (c >> 1) * 8 >= lim[nt][c & 1];
+                if (hidden) x[c] = 0.f;
+                if (!hidden) ol[nt][g][c & 1] = fmaf(pw[nt][c], lw[c >> 1], ol[nt][g][c & 1]);
+              } else {
+                ol[nt][g][c & 1] = fmaf(pw[nt][c], lw[c >> 1], ol[nt][g][c & 1]);
+              }
+            }
+            const uint32_t h0 = pack_half2(x[0], x[1]), h1 = pack_half2(x[2], x[3]);
+            const uint32_t b0 = transpose8(h0), b1 = transpose8(h1);
+            mma_f16(o[nt][g][0], f0, b0, b1);
+            mma_f16(o[nt][g][1], f1, b0, b1);
+            if constexpr (PARTS == 2) {
+              const __half2 k0 = *reinterpret_cast<const __half2*>(&h0);
+              const __half2 k1 = *reinterpret_cast<const __half2*>(&h1);
+              const uint32_t c0 = transpose8(pack_half2(x[0] - __low2float(k0), x[1] - __high2float(k0)));
+              const uint32_t c1 = transpose8(pack_half2(x[2] - __low2float(k1), x[3] - __high2float(k1)));
+              mma_f16(o[nt][g][0], f0, c0, c1);
+              mma_f16(o[nt][g][1], f1, c0, c1);
+            }
           }
         }
       }
     };
 
-    const int page_log = __ffs(page) - 1;
-    for (; (tile >> 3) - base_n < end - begin; tile += W) {
-      st += (tile >> 3) - stage;
-      stage = tile >> 3;
+    for (; tile / C::kTiles - base_n < end - begin; tile += kWarps) {
+      st += tile / C::kTiles - stage;
+      stage = tile / C::kTiles;
       if (st >= C::kStages) {
         st -= C::kStages;
         phase ^= 1;
@@ -777,13 +769,21 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
       if (ok) ok = mbar_wait_bounded(&full[st], phase, abort_flag, kTimeoutNs);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok) {
-        const int pg = (tile & 7) * kTile >> page_log, row = (tile & 7) * kTile & (page - 1);
-        const int pos = s_meta[st * 8 + pg] + row;
-        const unsigned char* base = smem + st * C::kStageBytes + pg * 2 * rec;
-        if (pos + kTile <= lim_min)
-          step(base, row, pos, std::false_type{});
-        else if (pos < lim_max)
-          step(base, row, pos, std::true_type{});
+        Tiles<TT> x;
+        bool all = true, some = false;
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+          const int at = tile % C::kTiles * C::kTile + tt * 16, pg = at >> page_log;
+          x.row[tt] = at & (page - 1);
+          x.pos[tt] = s_meta[st * 8 + pg] + x.row[tt];
+          x.base[tt] = smem + st * C::kStageBytes + pg * 2 * rec;
+          all = all && x.pos[tt] + 16 <= lim_min;
+          some = some || x.pos[tt] < lim_max;
+        }
+        if (all)
+          step(x, std::false_type{});
+        else if (some)
+          step(x, std::true_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
       }
@@ -805,14 +805,23 @@ __global__ void __launch_bounds__((W + 4) * 32, 1)
                           o[nt][g][1][c] * 0x1p24f, o[nt][g][1][2 + c] * 0x1p20f);
         }
       }
-      // lane (r, q) has row r of the sums for heads 2q and 2q + 1
+      // the sums over the lanes' tokens
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float* st = s_stat + (warp * ROWS + nt * 8 + 2 * q + c) * C::kStat;
-        if (r == 4) st[1] = ol[nt][c];
-        if (r < NG) st[2 + r] = ol[nt][c];
+        float x[NG + 1];
+        x[0] = l[nt][c];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) x[1 + g] = ol[nt][g][c];
+        float* dst = s_stat + (warp * ROWS + nt * 8 + 2 * q + c) * C::kStat;
+#pragma unroll
+        for (int g = 0; g <= NG; ++g) {
+          x[g] += __shfl_xor_sync(0xFFFFFFFFu, x[g], 4);
+          x[g] += __shfl_xor_sync(0xFFFFFFFFu, x[g], 8);
+          x[g] += __shfl_xor_sync(0xFFFFFFFFu, x[g], 16);
+          if (r == 0) dst[1 + g] = x[g];
+        }
+        if (r == 0) dst[0] = m[nt][c];
       }
-      if (q == 0) s_stat[(warp * ROWS + nt * 8 + r) * C::kStat] = m[nt];
     }
     consumers_sync<kWarps * 32>();
     const bool whole = begin == 0 && end == w.units;
@@ -896,16 +905,16 @@ __global__ void __launch_bounds__(D) kv4_join_kernel(const __grid_constant__ Par
     *dst = __float2bfloat16(acc * inv);
 }
 
-template <int D, int NT, int W, typename T>
+template <int D, int NT, typename T>
 int launch(const Params& p, cudaStream_t stream) {
-  using C = Cfg<D, NT, W>;
-  auto kern = kv4_attend_kernel<D, NT, W, T>;
+  using C = Cfg<D, NT>;
+  auto kern = kv4_attend_kernel<D, NT, T>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return SBSA_ERR_CUDA;
   int grid = sm_count();
   if (grid <= 0) return SBSA_ERR_CUDA;
   grid = grid < kMaxCtas ? grid : kMaxCtas;
-  kern<<<grid, C::kThreads, C::kSmem, stream>>>(p);
+  kern<<<grid, kThreads, C::kSmem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SBSA_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -937,10 +946,10 @@ int launch_kv4_attend(const Kv4AttendArgs& a, cudaStream_t stream) {
   // 16 rows share a read of the cache where a sequence has more than 8
   const bool two = (long long)p.group * a.max_new > 8;
   if (a.dtype == SBSA_FP32)
-    return a.d == 64 ? launch<64, 1, 8, float>(p, stream) : launch<128, 1, 8, float>(p, stream);
+    return a.d == 64 ? launch<64, 1, float>(p, stream) : launch<128, 1, float>(p, stream);
   if (a.d == 64)
-    return two ? launch<64, 2, 8, __nv_bfloat16>(p, stream) : launch<64, 1, 12, __nv_bfloat16>(p, stream);
-  return two ? launch<128, 2, 8, __nv_bfloat16>(p, stream) : launch<128, 1, 12, __nv_bfloat16>(p, stream);
+    return two ? launch<64, 2, __nv_bfloat16>(p, stream) : launch<64, 1, __nv_bfloat16>(p, stream);
+  return two ? launch<128, 2, __nv_bfloat16>(p, stream) : launch<128, 1, __nv_bfloat16>(p, stream);
 }
 
 }  // namespace sbsa
