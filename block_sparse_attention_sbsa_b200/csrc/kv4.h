@@ -52,9 +52,12 @@ struct Kv4AttendArgs {
   float sm_scale;
   void* workspace;
 };
-// Bytes of the partial results (see kv4_attend.cu).
-size_t kv4_attend_workspace(int d);
-// Returns an SBSA_* code.
-int launch_kv4_attend(const Kv4AttendArgs& a, cudaStream_t stream);
+// The two kernels of the attention, and the bytes of their partial results: for few
+// rows a sequence (all types, with lists), and for many (bf16, without lists).
+// The launchers return an SBSA_* code.
+size_t kv4_few_workspace(int d);
+int launch_kv4_few(const Kv4AttendArgs& a, cudaStream_t stream);
+size_t kv4_many_workspace(int d);
+int launch_kv4_many(const Kv4AttendArgs& a, cudaStream_t stream);
 
 }  // namespace sbsa

@@ -72,6 +72,13 @@ Kv4Batch batch(const sbsa_kv4_params* p, const int32_t* table, const int32_t* le
   return b;
 }
 
+// Which kernel: the one for many rows reads the cache once for 256 rows, the other one for
+// 16, but spends less on what it reads.
+bool many_rows(const sbsa_kv4_params* p) {
+  return p->dtype == SBSA_BF16 && !p->list_heads &&
+         (long long)p->max_new * (p->n_q_heads / p->n_kv_heads) > 32;
+}
+
 int cuda_code(cudaError_t e) { return e == cudaSuccess ? SBSA_OK : SBSA_ERR_CUDA; }
 
 }  // namespace
@@ -134,7 +141,7 @@ int sbsa_kv4_read(const sbsa_kv4_params* p, const void* cache, const int32_t* pa
 
 size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p) {
   if (validate_attend(p) != SBSA_OK) return 0;
-  return kv4_attend_workspace(p->head_dim);
+  return many_rows(p) ? kv4_many_workspace(p->head_dim) : kv4_few_workspace(p->head_dim);
 }
 
 int sbsa_kv4_attend(const sbsa_kv4_params* p, const void* cache, const int32_t* page_table,
@@ -173,7 +180,8 @@ int sbsa_kv4_attend(const sbsa_kv4_params* p, const void* cache, const int32_t* 
   a.max_blocks = p->max_blocks;
   a.sm_scale = p->sm_scale > 0.f ? p->sm_scale : 1.0f / std::sqrt((float)p->head_dim);
   a.workspace = workspace;
-  return launch_kv4_attend(a, static_cast<cudaStream_t>(stream));
+  auto launch = many_rows(p) ? launch_kv4_many : launch_kv4_few;
+  return launch(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

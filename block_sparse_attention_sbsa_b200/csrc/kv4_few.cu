@@ -36,7 +36,7 @@
 #include <type_traits>
 
 #include "internal.h"
-#include "kv4.cuh"
+#include "kv4_split.cuh"
 #include "ptx.cuh"
 #include "tma_map.h"
 
@@ -44,8 +44,9 @@ namespace sbsa {
 namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kUnit = 128;  // tokens of a stage
-constexpr int kMaxCtas = 160;
+constexpr int kUnit = kSplitUnit;  // tokens of a stage
+// What an item costs a CTA besides its units (rows, joining, output), in units.
+constexpr int kItemCost = 4;
 // Weights are 2^(S - M), M = (reference of the logits) + (reference of the
 // values' exponents) - kHead; each reference moves only when it is outgrown by more
 // than kLazy, so the fp16 weights times a scale stay below 2^(kHead + 2 kLazy + 1) = 2^15.
@@ -76,95 +77,13 @@ struct Cfg {
   static constexpr int kStat = 2 + kGroups;
   static constexpr int kOffMeta = kOffStat + kWarps * kRows * kStat * 4;
   static constexpr int kOffScan = kOffMeta + kStages * 8 * 4;
-  static constexpr int kOffBar = kOffScan + (kThreads / 32 + 1) * 8 + 32;
+  static constexpr int kOffBar = kOffScan + kScanBytes<kThreads>;
   static constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
 };
 
-struct Part {  // which item's first part a CTA holds, in how many parts (0: none)
-  int parts, seq, head, tile;
-};
-
-constexpr int slot_floats(int d) { return 16 * (d + 2); }
-
-struct Params {
-  Kv4AttendArgs a;
-  int heads;         // items per sequence and row tile: kv heads, or listed query heads
-  int group;         // query heads of an item
-  int kv_div;        // item head / kv_div = kv head
-  float scale_log2;  // sm_scale * log2(e)
-  float* slots;
-  Part* parts;
-};
-
-// The sequence as an item sees it.
-struct Seq {
-  int first, rows, len;  // first row, number of rows, tokens
-};
-
-__device__ __forceinline__ Seq seq_of(const Params& p, int b) {
-  Seq s;
-  const int lo = clamp_int(p.a.b.cu[b], 0, p.a.b.n_tokens);
-  const int hi = clamp_int(p.a.b.cu[b + 1], lo, p.a.b.n_tokens);
-  s.first = lo;
-  s.rows = hi - lo;
-  s.len = kv4_len(p.a.b, b);
-  return s;
-}
-
-// What an item costs a CTA besides its units (rows, joining, output), in units.  Runs are
-// cut by cost: item after item, kItemCost and then the units.
-constexpr int kItemCost = 4;
-
-// Units of 128 tokens of each row tile of (sequence, head) and the number of
-// tiles; a tile that sees nothing still takes one unit (it writes zeros).
-template <int ROWS>
-__device__ __forceinline__ void item_size(const Params& p, int b, int head, int* units,
-                                          int* tiles) {
-  const Seq s = seq_of(p, b);
-  *tiles = (int)(((long long)s.rows * p.group + ROWS - 1) / ROWS);
-  int n = s.len;
-  if (p.a.list_heads)
-    n = clamp_int(p.a.cnt[(long long)b * p.heads + head], 0, p.a.max_blocks) * p.a.block;
-  n = (n + kUnit - 1) / kUnit;
-  *units = n < 1 ? 1 : n;
-}
-
-// The CTA's place in the sequence of items.
-struct Walk {
-  int b, head, tile;   // current item
-  int units, tiles;    // its units, its sequence's tiles
-  long long cost;      // cost from the item's start to the run's first
-  long long left;      // and to the run's end
-  // units of the item that are the CTA's: [begin, end), empty where the run ends before the first
-  __device__ int begin() const { return cost > kItemCost ? (int)cost - kItemCost : 0; }
-  __device__ int end() const {
-    const long long e = left - kItemCost;
-    return e < 0 ? 0 : e < units ? (int)e : units;
-  }
-};
-
-__device__ __forceinline__ long long units_cost(int units) { return (long long)kItemCost + units; }
-
-template <int ROWS>
-__device__ __forceinline__ void next_item(const Params& p, Walk& w) {
-  w.left -= units_cost(w.units);
-  w.cost = 0;
-  if (w.left <= 0) return;
-  if (++w.tile < w.tiles) return;
-  w.tile = 0;
-  do {
-    if (++w.head == p.heads) {
-      w.head = 0;
-      if (++w.b == p.a.b.n_seqs) {
-        w.left = 0;
-        return;
-      }
-    }
-    item_size<ROWS>(p, w.b, w.head, &w.units, &w.tiles);
-  } while (w.tiles == 0);
-}
+constexpr int kSlotRows = 16;
 
 // D += A B on fp16, 16 x 16 by 16 x 8; and D = A B.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -262,16 +181,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
-// Row r of a tile: the token row and head of o (and q); false past the last.
-__device__ __forceinline__ bool row_of(const Params& p, const Seq& s, int head, long long row,
-                                       long long* t, int* h, int* i) {
-  *i = (int)(row / p.group);
-  if (*i >= s.rows) return false;
-  *t = s.first + *i;
-  *h = head * p.group + (int)(row % p.group);
-  return true;
-}
-
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -282,7 +191,7 @@ __device__ __forceinline__ void consumers_sync() {
 // elements are scaled by a power of two so that the largest is near 2^10) and
 // the weights are rounded to fp16 once, 2^-11 of each.
 template <int D, int NT, typename T>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_constant__ SplitParams p) {
   using C = Cfg<D, NT>;
   constexpr int NG = C::kGroups;
   constexpr int ROWS = C::kRows;
@@ -293,30 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   float* s_stat = reinterpret_cast<float*>(smem + C::kOffStat);
   int* s_meta = reinterpret_cast<int*>(smem + C::kOffMeta);  // [stage][page]: first token's position
   long long* s_scan = reinterpret_cast<long long*>(smem + C::kOffScan);
-  int* s_start = reinterpret_cast<int*>(s_scan + kThreads / 32 + 1);  // b, head, tile, unit, abort
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* empty = full + C::kStages;
-  volatile int* abort_flag = s_start + 4;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int page = p.a.b.page, rec = kv4_rec_bytes(page, D);
 
-  // ---- the CTA's run of units: a scan over the items' sizes
-  const int items = p.a.b.n_seqs * p.heads;
-  const int per = (items + kThreads - 1) / kThreads;
-  const int i0 = min(items, (int)threadIdx.x * per), i1 = min(items, i0 + per);
-  long long mine = 0;
-  for (int i = i0; i < i1; ++i) {
-    int units, tiles;
-    item_size<ROWS>(p, i / p.heads, i % p.heads, &units, &tiles);
-    mine += units_cost(units) * tiles;
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-    if (lane >= m) incl += x;
-  }
-  if (lane == 31) s_scan[warp] = incl;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -325,39 +216,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     *abort_flag = 0;
     fence_barrier_init();
   }
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+  Run run;
+  if (!split_run<ROWS, kItemCost, kThreads>(p, s_scan, &run)) return;
+  SplitWalk<ROWS, kItemCost> w(p, run);
   const int cta = blockIdx.x;
-  if (threadIdx.x == 0) p.parts[cta].parts = 0;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (cta >= ctas) return;
-  const long long u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
-  if (u0 >= before && u0 < before + mine) {
-    long long x = before;
-    for (int i = i0; i < i1; ++i) {
-      int units, tiles;
-      item_size<ROWS>(p, i / p.heads, i % p.heads, &units, &tiles);
-      if (u0 < x + units_cost(units) * tiles) {
-        s_start[0] = i / p.heads;
-        s_start[1] = i % p.heads;
-        s_start[2] = (int)((u0 - x) / units_cost(units));
-        s_start[3] = (int)((u0 - x) % units_cost(units));
-        break;
-      }
-      x += units_cost(units) * tiles;
-    }
-  }
-  __syncthreads();
-  Walk w;
-  w.b = s_start[0], w.head = s_start[1], w.tile = s_start[2], w.cost = s_start[3];
-  w.left = w.cost + u1 - u0;
-  item_size<ROWS>(p, w.b, w.head, &w.units, &w.tiles);
 
   auto fail = [&]() {
     *abort_flag = 1;
@@ -371,12 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     const int pages = kUnit / page;
     int n = 0;  // stages filled
     bool ok = true;
-    while (w.left > 0 && ok) {
-      const Seq s = seq_of(p, w.b);
+    for (; w.more() && ok; w.next(p)) {
+      const Seq s = w.seq;
       const int begin = w.begin(), end = w.end();
-      // tokens that the tile's last row sees
-      const long long last = min((long long)(w.tile + 1) * ROWS, (long long)s.rows * p.group) - 1;
-      const int limit = s.len - s.rows + (int)(last / p.group) + 1;
+      const int limit = w.limit();
       const int32_t* list = nullptr;
       int count = 0;
       if (p.a.list_heads) {
@@ -434,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
                     heads + (long long)pg * p.a.b.hkv * 2 * rec, 2 * rec, &full[st]);
         ++n;
       }
-      next_item<ROWS>(p, w);
     }
     if (!ok && lane == 0) {
       if (!*abort_flag) fail();
@@ -458,10 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   int base_n = 0;                    // the number of the item's first stage
   const int page_log = __ffs(page) - 1;
   bool ok = true;
-  while (w.left > 0) {
-    const Seq s = seq_of(p, w.b);
+  for (; w.more(); w.next(p)) {
+    const Seq s = w.seq;
     const int begin = w.begin(), end = w.end();
-    if (begin >= end) break;  // the run ends in the item's fixed cost: the next CTA begins it
     const long long row0 = (long long)w.tile * ROWS;
 
     // ---- the query rows as fragments: elements (0, 4), (1, 5)/16, (2, 6), (3, 7)/16 of each 8
@@ -824,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       }
     }
     consumers_sync<kWarps * 32>();
-    const bool whole = begin == 0 && end == w.units;
+    const bool whole = w.whole();
     const int slot = 2 * cta + (begin == 0 ? 1 : 0);
     constexpr int kPerRow = D / 4;  // threads of a row, 4 channels each
     for (int x = threadIdx.x; x < ROWS * kPerRow; x += kWarps * 32) {
@@ -854,59 +712,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         }
       } else {
-        float* dst = p.slots + (long long)slot * slot_floats(D);
+        float* dst = p.slots + (long long)slot * slot_floats(kSlotRows, D);
         *reinterpret_cast<float4*>(dst + row * D + c) = acc;
         if (c == 0) {
-          dst[16 * D + row] = top;
-          dst[16 * D + 16 + row] = sum;
+          dst[kSlotRows * D + row] = top;
+          dst[kSlotRows * (D + 1) + row] = sum;
         }
       }
     }
-    if (!whole && begin == 0 && threadIdx.x == 0) {
-      // the item goes on in the CTAs up to the one that owns its last unit
-      const long long last = u1 - w.left + units_cost(w.units) - 1;
-      const int owner = (int)(((last + 1) * ctas + total - 1) / total) - 1;
-      p.parts[cta] = Part{owner - cta + 1, w.b, w.head, w.tile};
-    }
-    next_item<ROWS>(p, w);
+    if (!whole && begin == 0 && threadIdx.x == 0) p.parts[cta] = w.part(run, cta);
   }
 }
 
-// Joins the parts of the item that begins in CTA blockIdx.x and goes on in
-// the next ones; one CTA a row, one thread a channel.
 template <int D, int NT, typename T>
-__global__ void __launch_bounds__(D) kv4_join_kernel(const __grid_constant__ Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Part part = p.parts[blockIdx.x];
-  if (part.parts < 2) return;
-  const int row = blockIdx.y, c = threadIdx.x;
-  const Seq s = seq_of(p, part.seq);
-  long long t;
-  int h, i;
-  if (!row_of(p, s, part.head, (long long)part.tile * 8 * NT + row, &t, &h, &i)) return;
-  auto slot = [&](int k) {
-    return p.slots + (long long)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * slot_floats(D);
-  };
-  float top = -FLT_MAX;
-  for (int k = 0; k < part.parts; ++k) top = fmaxf(top, slot(k)[16 * D + row]);
-  float acc = 0.f, sum = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < part.parts; ++k) {
-    const float* x = slot(k);
-    const float fac = exp2f(x[16 * D + row] - top);
-    sum = fmaf(fac, x[16 * D + 16 + row], sum);
-    acc = fmaf(fac, x[row * D + c], acc);
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  T* dst = static_cast<T*>(p.a.o) + t * p.a.o_token + h * p.a.o_head + c;
-  if constexpr (sizeof(T) == 4)
-    *dst = acc * inv;
-  else
-    *dst = __float2bfloat16(acc * inv);
-}
-
-template <int D, int NT, typename T>
-int launch(const Params& p, cudaStream_t stream) {
+int launch(const SplitParams& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   auto kern = kv4_attend_kernel<D, NT, T>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
@@ -916,33 +735,15 @@ int launch(const Params& p, cudaStream_t stream) {
   grid = grid < kMaxCtas ? grid : kMaxCtas;
   kern<<<grid, kThreads, C::kSmem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SBSA_ERR_CUDA;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, 8 * NT);
-  cfg.blockDim = dim3(D);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, T>, p) == cudaSuccess ? SBSA_OK : SBSA_ERR_CUDA;
+  return launch_join<D, 8 * NT, kSlotRows, false, T>(p, grid, stream);
 }
 
 }  // namespace
 
-size_t kv4_attend_workspace(int d) {
-  return kMaxCtas * (2 * slot_floats(d) * sizeof(float) + sizeof(Part));
-}
+size_t kv4_few_workspace(int d) { return split_workspace(kSlotRows, d); }
 
-int launch_kv4_attend(const Kv4AttendArgs& a, cudaStream_t stream) {
-  Params p{};
-  p.a = a;
-  p.heads = a.list_heads ? a.list_heads : a.b.hkv;
-  p.group = a.hq / p.heads;
-  p.kv_div = p.heads / a.b.hkv;
-  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
-  p.slots = static_cast<float*>(a.workspace);
-  p.parts = reinterpret_cast<Part*>(p.slots + (size_t)kMaxCtas * 2 * slot_floats(a.d));
+int launch_kv4_few(const Kv4AttendArgs& a, cudaStream_t stream) {
+  const SplitParams p = split_params(a, kSlotRows);
   // 16 rows share a read of the cache where a sequence has more than 8
   const bool two = (long long)p.group * a.max_new > 8;
   if (a.dtype == SBSA_FP32)

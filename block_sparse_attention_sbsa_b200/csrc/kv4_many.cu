@@ -1,0 +1,641 @@
+// Attention over the 4-bit key-value cache for many rows (chunks of prompts),
+// bf16, on tcgen05.
+//
+// Mathematics.  Keys and values are taken back to fp16 once a tile of 128 tokens
+// and used for 256 rows (two query tiles A and B of 128: tokens by query heads of a
+// kv head): S = Q K^T, exact online softmax, O += P V.  In fp16 a value stands for
+// (low' + scale' n), with low' and scale' scaled by a power of two common to the tile
+// so that both stay below 2^-8: a level in the low bits of a half is the fp16 denormal
+// n 2^-24, and one fused multiply-add by scale' 2^24 (2^20 where the level stands at bit
+// 4) gives the value, rounded once, 2^-11 of it (2^-21 of the tile's largest for those far
+// below).  q's rows are scaled to fp16 exactly.  The powers of two go into the logits'
+// factor and, for the values, into O's rescaling.
+//
+// Bound: the tensor cores and the exponentials alike.  A tile of 128 tokens against 256
+// rows is 2 * 2 * 2^21 multiply-adds, 2096 cycles at 4000 a cycle, its 2^15 exponentials
+// 2048 cycles at 16 a cycle; unpacking takes about 450 instructions a dequantising warp.
+//
+// One CTA an SM, 16 warps:
+//   0-3, 4-7  softmax of tile A, of tile B: a thread has a row; S out of TMEM, P (fp16)
+//             back over its first half; the reference maximum moves (and O is
+//             rescaled in TMEM) only when it is outgrown by 2^8.  They write their
+//             tile's Q into shared memory and O to global memory.
+//   8-11      a thread has a token of the tile: reads its levels from global memory
+//             one tile ahead and writes its K and V rows into the swizzled layout of
+//             the products' operands (two buffers each; the channels in the order in
+//             which they come out of the words, which Q and the output follow).
+//   12        issues the products: [PV_A(j-1), S_A(j)], [PV_B(j-1), S_B(j)], ...; one
+//             commit each announces S, that the O of the tile is at rest, and (B's) that
+//             K(j) and V(j-1) are free again.
+// The items and their cut over the CTAs: kv4_split.cuh.  Every wait is bounded (2 s).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <climits>
+
+#include "internal.h"
+#include "kv4_split.cuh"
+#include "ptx.cuh"
+
+namespace sbsa {
+namespace {
+
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kRows = 256;  // of an item: two tiles of 128
+constexpr int kItemCost = 2;
+constexpr int kThreads = 512;
+// 256 * 184 + 128 * 96 + 128 * 48 = 512 * 128, what the block is launched with
+constexpr int kRegsSoftmax = 184, kRegsUnpack = 96, kRegsIssue = 48;
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int D>
+struct MC {
+  static constexpr int NG = D / 32;
+  static constexpr int kTileBytes = 128 * D * 2;   // of Q, K or V
+  static constexpr int kOffQ = 0;                  // Q[2]
+  static constexpr int kOffK = 2 * kTileBytes;     // K[2]
+  static constexpr int kOffV = 4 * kTileBytes;     // V[2]
+  static constexpr int kOffInfo = 6 * kTileBytes;  // Info[4]
+  static constexpr int kInfoBytes = 32;
+  static constexpr int kOffNan = kOffInfo + 4 * kInfoBytes;  // int[4 items][4 groups]
+  static constexpr int kOffMax = kOffNan + 64;               // uint32[2 parities][4 warps][2]
+  static constexpr int kOffScan = kOffMax + 64;
+  static constexpr int kOffBar = kOffScan + kScanBytes<kThreads>;
+  // q_full[2] k_full[2] v_full[2] s_bar[2][2] o_bar[2][2] p_full[2] drain
+  static constexpr int kBars = 2 + 2 + 2 + 4 + 4 + 2 + 1;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
+  static constexpr int kSmem = kOffMisc + 16 + 1024;
+  static constexpr uint32_t kDescS = make_idesc(0, 128, 128, false, false);
+  static constexpr uint32_t kDescO = make_idesc(0, 128, D, false, true);
+  static constexpr int kTmO = 256;  // TMEM: S_A, S_B (128 columns each), O_A, O_B (D each)
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kOffScan % 8 == 0 && kOffBar % 8 == 0, "alignment");
+};
+
+// What the softmax has to know of a tile of tokens.
+struct Info {
+  float k_exp;       // logits are S' * 2^k_exp * the row's factor
+  int v_exp;         // O's unit after this tile: 2^v_exp
+  uint32_t on[4];    // tokens whose page is in the cache
+  int pad[2];
+};
+static_assert(sizeof(Info) == 32, "Info");
+
+__device__ __forceinline__ uint32_t h2(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+
+// Eight channels of a word of levels as fp16 values, in the order 0 4 1 5 2 6 3 7:
+// the halves hold channels i and i + 4, with scale (2^24, and 2^20 for the odd i) and low.
+__device__ __forceinline__ uint4 unpack8(uint32_t x, __half2 se, __half2 so, __half2 lo) {
+  const uint32_t y = x >> 8;
+  uint4 r;
+  r.x = h2(__hfma2(as_h2(x & 0x000F000Fu), se, lo));
+  r.y = h2(__hfma2(as_h2(x & 0x00F000F0u), so, lo));
+  r.z = h2(__hfma2(as_h2(y & 0x000F000Fu), se, lo));
+  r.w = h2(__hfma2(as_h2(y & 0x00F000F0u), so, lo));
+  return r;
+}
+
+// Offset of chunk c (8 elements) of row `row` in a tile of 128 rows.
+__device__ __forceinline__ int chunk_at(int row, int c) {
+  return (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_constant__ SplitParams p) {
+  using C = MC<D>;
+  constexpr int NG = C::NG;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* q_full = bar;          // [tile]
+  uint64_t* k_full = bar + 2;      // [token tile & 1]
+  uint64_t* v_full = bar + 4;
+  uint64_t* s_bar = bar + 6;       // [tile * 2 + (token tile & 1)]: S(j) and PV(j - 1) done
+  uint64_t* o_bar = bar + 10;      // [tile * 2 + (item & 1)]: the item's last PV done
+  uint64_t* p_full = bar + 14;     // [tile]
+  uint64_t* drain = bar + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  Info* info = reinterpret_cast<Info*>(smem + C::kOffInfo);
+  int* nan_pos = reinterpret_cast<int*>(smem + C::kOffNan);
+  uint32_t* s_max = reinterpret_cast<uint32_t*>(smem + C::kOffMax);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&k_full[i], 128);
+      mbar_init(&v_full[i], 128);
+      mbar_init(&p_full[i], 128);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_bar[i], 1);
+      mbar_init(&o_bar[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  Run run;
+  if (!split_run<kRows, kItemCost, kThreads>(p, reinterpret_cast<long long*>(smem + C::kOffScan), &run))
+    return;
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int cta = blockIdx.x;
+  SplitWalk<kRows, kItemCost> w(p, run);
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    if (p.a.b.status) atomicCAS(p.a.b.status, 0, SBSA_ERR_TIMEOUT);
+  };
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    return mbar_wait_bounded(b, parity, abort_flag, kTimeoutNs);
+  };
+  // rows of the item (past the last sequence row: none) and whether it has a tile B
+  auto item_rows = [&]() {
+    return (int)min((long long)kRows, (long long)w.seq.rows * p.group - (long long)w.tile * kRows);
+  };
+
+  if (warp < 8) {
+    // ================================================================ softmax
+    regs_raise<kRegsSoftmax>();
+    const int x = warp >> 2;  // which tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + x * 128;
+    const uint32_t o_col = tmem + lanes + C::kTmO + x * D;
+    int n = 0, item = 0;  // token tiles and items so far
+    bool ok = true;
+    for (; w.more() && ok; w.next(p), ++item) {
+      const int begin = w.begin(), end = w.end();
+      const int rows = item_rows();
+      if (x == 1 && rows <= 128) {
+        // no tile B: its warps keep in step with its barriers (a wait for a phase that is more
+        // than one away from the current one would take one for the other)
+        for (int j = begin; ok && j < end; ++j, ++n) {
+          ok = __all_sync(0xFFFFFFFFu, wait(&s_bar[2 + (n & 1)], (n >> 1) & 1));
+          if (ok) mbar_arrive(&p_full[1]);
+        }
+        if (ok) ok = __all_sync(0xFFFFFFFFu, wait(&o_bar[2 + (item & 1)], (item >> 1) & 1));
+        continue;
+      }
+      long long t = 0;
+      int h = 0, i = 0;
+      const bool have = row_of(p, w.seq, w.head, (long long)w.tile * kRows + x * 128 + row, &t, &h, &i);
+      // ---- Q: the row in fp16, scaled by a power of two to a largest element near 2^10
+      const int visible = w.seq.len - w.seq.rows + i + 1;
+      int lim = w.limit();  // rows past the last see all, so that they never mask
+      if (have) {
+        lim = i < p.a.max_new ? max(visible, 0) : 0;
+        if (visible < 1 || i >= p.a.max_new) kv4_record(p.a.b.status);
+      }
+      float f;
+      {
+        uint4 u[D / 8];
+        float mx = 0.f;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.a.q.ptr) + t * p.a.q.token + h * p.a.q.head);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          u[c] = have ? src[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t v[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v[k] << 16)),
+                                 fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
+        }
+        const int e = clamp_int(137 - (int)(__float_as_uint(mx) >> 23), -90, 100);
+        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+        f = p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+        unsigned char* dst = smem + C::kOffQ + x * C::kTileBytes;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {  // 8 channels 32 g + 8 q: chunk q NG + g
+          const uint32_t v[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+          float z[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            z[2 * k] = __uint_as_float(v[k] << 16) * up;
+            z[2 * k + 1] = __uint_as_float(v[k] & 0xFFFF0000u) * up;
+          }
+          uint4 o;
+          o.x = h2(__floats2half2_rn(z[0], z[4]));
+          o.y = h2(__floats2half2_rn(z[1], z[5]));
+          o.z = h2(__floats2half2_rn(z[2], z[6]));
+          o.w = h2(__floats2half2_rn(z[3], z[7]));
+          *reinterpret_cast<uint4*>(dst + chunk_at(row, (c & 3) * NG + (c >> 2))) = o;
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();  // O of the item before has been read
+      mbar_arrive(&q_full[x]);
+
+      float m = -FLT_MAX, l = 0.f;
+      int v_exp = INT_MIN;
+      for (int j = begin; j < end; ++j, ++n) {
+        ok = __all_sync(0xFFFFFFFFu, wait(&s_bar[x * 2 + (n & 1)], (n >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const Info& in = info[n & 3];
+        const float c = f * exp2f(in.k_exp);
+        const int ve = in.v_exp;
+        float s[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tmem_ld32(s_col + k * 32, *reinterpret_cast<float(*)[32]>(s + k * 32));
+        tmem_wait_ld();
+        const uint32_t on = in.on[0] & in.on[1] & in.on[2] & in.on[3];
+        if (__any_sync(0xFFFFFFFFu, j * 128 + 128 > lim) || on != 0xFFFFFFFFu) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int left = lim - j * 128 - k * 32;  // of these 32 tokens the row sees so many
+            uint32_t bits = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+            bits &= in.on[k];
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!((bits >> y) & 1u)) s[k * 32 + y] = -INFINITY;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 128; k += 4) {
+          mx[0] = fmaxf(mx[0], s[k]);
+          mx[1] = fmaxf(mx[1], s[k + 1]);
+          mx[2] = fmaxf(mx[2], s[k + 2]);
+          mx[3] = fmaxf(mx[3], s[k + 3]);
+        }
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
+        if (j == begin) {
+          m = mn;
+          v_exp = ve;
+        } else if (__any_sync(0xFFFFFFFFu, mn > m + kRescaleLog2) || ve != v_exp) {
+          // (S(j)'s commit says that O holds PV(j - 1))
+          const float alpha = exp2f(m - mn);
+          l *= alpha;
+          m = mn;
+          const float ao = alpha * exp2f((float)(v_exp - ve));
+          v_exp = ve;
+#pragma unroll
+          for (int k = 0; k < D; k += 16) {
+            float o[16];
+            tmem_ld16(o_col + k, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] *= ao;
+            tmem_st16(o_col + k, o);
+          }
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            const float p0 = ex2_approx(fmaf(s[k * 32 + y], c, -m));
+            const float p1 = ex2_approx(fmaf(s[k * 32 + y + 1], c, -m));
+            sum[0] += p0;
+            sum[1] += p1;
+            pk[y >> 1] = h2(__floats2half2_rn(p0, p1));
+          }
+          tmem_st16u(s_col + k * 16, pk);
+        }
+        l += sum[0] + sum[1];
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      // ---- O
+      ok = __all_sync(0xFFFFFFFFu, wait(&o_bar[x * 2 + (item & 1)], (item >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = w.whole();
+      const int* np = nan_pos + (item & 3) * 4;
+      float* slot = p.slots + (size_t)(2 * cta + (begin == 0 ? 1 : 0)) * slot_floats(kRows, D);
+      const int sr = x * 128 + row;
+      // powers of two of the values' unit, in two steps (each within fp32's range)
+      const float u0 = exp2f((float)(v_exp >> 1)), u1 = exp2f((float)(v_exp - (v_exp >> 1)));
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.o) + t * p.a.o_token + h * p.a.o_head;
+#pragma unroll
+      for (int k = 0; k < D; k += 32) {
+        float o[32];
+        tmem_ld32(o_col + k, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          // place k + y: group 2 (chunk & 1) + (y & 1) with 4 groups, y & 1 with 2
+          const int g = NG == 4 ? 2 * ((y >> 3) & 1) + (y & 1) : (y & 1);
+          o[y] = lim > np[g] ? NAN : o[y] * inv * u0 * u1;
+        }
+        if (!whole) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 4)
+            *reinterpret_cast<float4*>(slot + (size_t)sr * D + k + y) =
+                make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+        } else if (have) {
+          // 32 places are 32 / NG channels of each group, beginning at 4 r of the first chunk
+          constexpr int kPer = 32 / NG;
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int y = 0; y < kPer; y += 8) {
+              uint32_t b[4];
+#pragma unroll
+              for (int z = 0; z < 8; z += 2) {
+                // channel y + z of these: chunk of r = (y + z) / 4, place 2 (channel % 4) + (g & 1)
+                const int c0 = y + z;
+                const int at = NG == 4 ? (c0 >> 2) * 16 + (g >> 1) * 8 + 2 * (c0 & 3) + (g & 1)
+                                       : (c0 >> 2) * 8 + 2 * (c0 & 3) + g;
+                const __nv_bfloat162 v = __floats2bfloat162_rn(o[at], o[at + 2]);
+                b[z >> 1] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              *reinterpret_cast<uint4*>(dst + 32 * g + k / NG + y) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+        }
+      }
+      if (!whole) {
+        slot[(size_t)kRows * D + sr] = m;
+        slot[(size_t)kRows * (D + 1) + sr] = l;
+        if (begin == 0 && threadIdx.x == 0) p.parts[cta] = w.part(run, cta);
+      }
+      tc_fence_before();
+    }
+    if (!ok && lane == 0 && !*abort_flag) fail();
+  } else if (warp < 12) {
+    // ================================================================ tokens
+    regs_lower<kRegsUnpack>();
+    const int tok = threadIdx.x - 256;
+    const int page = p.a.b.page, page_log = __ffs(page) - 1, rec = kv4_rec_bytes(page, D);
+    constexpr int kWords = D / 32;  // 16-byte pieces of a row of levels
+    int n = 0, item = 0;
+
+    int ended[2] = {0, 0};  // by buffer: 1 + the item that ended with its last token tile, else 0
+    bool ok = true;
+    for (; w.more() && ok; w.next(p), ++item) {
+      const int begin = w.begin(), end = w.end(), limit = w.limit();
+      const int32_t* table = p.a.b.table + (long long)w.b * p.a.b.max_pages;
+      const uint8_t* heads = p.a.cache + (long long)w.head * 2 * rec;
+      // this thread's token of token tile j: its page number, -1 behind the last token, -2 where the
+      // page is not in the cache
+      auto look = [&](int j) {
+        const int pos = j * 128 + tok;
+        if (j >= end || pos >= limit) return -1;
+        const int pg = table[pos >> page_log];
+        return pg < 0 || pg >= p.a.b.n_pages ? -2 : pg;
+      };
+      auto keys = [&](int pg) { return heads + (long long)pg * p.a.b.hkv * 2 * rec; };
+      const int off = tok & (page - 1);
+      const int turn = NG == 4 ? ((off >> 1) & 1) * 2 : 0;  // 16-byte pieces of a value's row change places
+      uint4 kw[kWords], vw[kWords], kp, vp, kp2, vp2;
+      auto load_pairs = [&](int pg, uint4& a, uint4& b) {
+        a = b = make_uint4(0, 0, 0, 0);
+        if (pg < 0) return;
+        const uint8_t* src = keys(pg) + page * (D / 2) + off * (D / 8);
+        if constexpr (NG == 4) {
+          a = *reinterpret_cast<const uint4*>(src);
+          b = *reinterpret_cast<const uint4*>(src + rec);
+        } else {
+          const uint2 a2 = *reinterpret_cast<const uint2*>(src), b2 = *reinterpret_cast<const uint2*>(src + rec);
+          a = make_uint4(a2.x, a2.y, 0, 0);
+          b = make_uint4(b2.x, b2.y, 0, 0);
+        }
+      };
+      auto load_keys = [&](int pg) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+          kw[i] = pg < 0 ? make_uint4(0, 0, 0, 0)
+                         : reinterpret_cast<const uint4*>(keys(pg) + off * (D / 2))[i];
+      };
+      auto load_values = [&](int pg) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+          vw[i] = pg < 0 ? make_uint4(0, 0, 0, 0)
+                         : reinterpret_cast<const uint4*>(keys(pg) + rec + off * (D / 2))[i ^ turn];
+      };
+      int pg = look(begin), pg2 = look(begin + 1);
+      load_pairs(pg, kp, vp);
+      load_keys(pg);
+      load_values(pg);
+      uint32_t ve = 47;  // the values' exponent so far (as bf16 holds it; at least 2^-80)
+      if (tok < 4) nan_pos[(item & 3) * 4 + tok] = INT_MAX;
+      for (int j = begin; j < end; ++j, ++n) {
+        const int pg3 = look(j + 2);
+        load_pairs(pg2, kp2, vp2);
+        // ---- the tile's exponents: of the largest scale or low of its keys, of its values
+        uint32_t ka = 0, va = 0;
+        const uint32_t pk[4] = {kp.x, kp.y, kp.z, kp.w}, pv[4] = {vp.x, vp.y, vp.z, vp.w};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t a = pk[g] & 0x7FFFu, b = (pk[g] >> 16) & 0x7FFFu;
+          const uint32_t c = pv[g] & 0x7FFFu, d = (pv[g] >> 16) & 0x7FFFu;
+          ka = max(ka, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+          va = max(va, max(c < 0x7F80u ? c : 0u, d < 0x7F80u ? d : 0u));
+        }
+        ka = __reduce_max_sync(0xFFFFFFFFu, ka);
+        va = __reduce_max_sync(0xFFFFFFFFu, va);
+        uint32_t* mx = s_max + (n & 1) * 8;
+        if (lane == 0) {
+          mx[(warp - 8) * 2] = ka;
+          mx[(warp - 8) * 2 + 1] = va;
+        }
+        if (bar_red_or(1, 128, !ok)) {
+          ok = false;
+          break;
+        }
+        ka = max(max(mx[0], mx[2]), max(mx[4], mx[6]));
+        va = max(max(mx[1], mx[3]), max(mx[5], mx[7]));
+        const uint32_t ke = max(ka >> 7, 47u);
+        ve = max(ve, va >> 7);
+        // scales and lows below 2^-8: times 2^-(e + 9)
+        const int kn = (int)ke - 127 + 9, vn = (int)ve - 127 + 9;
+        const uint32_t on = __ballot_sync(0xFFFFFFFFu, pg != -2);
+        if (pg == -2) kv4_record(p.a.b.status);
+        // ---- K(n), once S(n - 2) has been taken of its buffer
+        if (ok && n >= 2) ok = wait(&s_bar[2 + (n & 1)], ((n - 2) >> 1) & 1);
+        if (ok) {
+          Info& in = info[n & 3];
+          if (tok == 0) {
+            in.k_exp = (float)kn;
+            in.v_exp = vn;
+          }
+          if (lane == 0) in.on[warp - 8] = on;
+          unsigned char* dst = smem + C::kOffK + (n & 1) * C::kTileBytes;
+          // 2^(24 - kn), in two factors (either may leave fp32's range alone)
+          const float a0 = exp2f((float)((24 - kn) >> 1)), a1 = exp2f((float)(24 - kn - ((24 - kn) >> 1)));
+          __half2 se[NG], so[NG], lo[NG];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float sc = __uint_as_float(pk[g] << 16) * a0 * a1;
+            const float lw = __uint_as_float(pk[g] & 0xFFFF0000u) * a0 * a1 * 0x1p-24f;
+            se[g] = __float2half2_rn(sc);
+            so[g] = __float2half2_rn(sc * 0.0625f);
+            lo[g] = __float2half2_rn(lw);
+          }
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {  // d = 128: piece q, words g; d = 64: two pieces of two
+            const uint32_t wd[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(dst + chunk_at(tok, i * 4 + k)) =
+                  unpack8(wd[k], se[k % NG], so[k % NG], lo[k % NG]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&k_full[n & 1]);
+        }
+        load_keys(pg2);
+        // ---- V(n), once PV(n - 2) has: with S(n - 1) in the same item, or the item's last PV
+        if (ok && n >= 2) {
+          const int it = ended[n & 1];
+          ok = it ? wait(&o_bar[2 + ((it - 1) & 1)], ((it - 1) >> 1) & 1)
+                  : wait(&s_bar[2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1);
+        }
+        if (ok) {
+          unsigned char* dst = smem + C::kOffV + (n & 1) * C::kTileBytes;
+          const float a0 = exp2f((float)((24 - vn) >> 1)), a1 = exp2f((float)(24 - vn - ((24 - vn) >> 1)));
+          float sc[NG], lw[NG];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            sc[g] = __uint_as_float(pv[g] << 16) * a0 * a1;
+            lw[g] = __uint_as_float(pv[g] & 0xFFFF0000u) * a0 * a1 * 0x1p-24f;
+            // a NaN group stands as 0 in the products (rows that do not see the token must not
+            // meet it); the rows that do get their NaN at the end
+            if ((pv[g] & 0x7F80u) == 0x7F80u || (pv[g] & 0x7F800000u) == 0x7F800000u) {
+              sc[g] = lw[g] = 0.f;
+              atomicMin(&nan_pos[(item & 3) * 4 + g], j * 128 + tok);
+            }
+          }
+          __half2 se[NG / 2], so[NG / 2], lo[NG / 2];
+#pragma unroll
+          for (int g = 0; g < NG / 2; ++g) {
+            se[g] = __floats2half2_rn(sc[2 * g], sc[2 * g + 1]);
+            so[g] = __floats2half2_rn(sc[2 * g] * 0.0625f, sc[2 * g + 1] * 0.0625f);
+            lo[g] = __floats2half2_rn(lw[2 * g], lw[2 * g + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            const uint32_t wd[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(dst + chunk_at(tok, i * 4 + k)) =
+                  unpack8(wd[k], se[k % (NG / 2)], so[k % (NG / 2)], lo[k % (NG / 2)]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&v_full[n & 1]);
+        }
+        load_values(pg2);
+        ended[n & 1] = j == end - 1 ? item + 1 : 0;
+        kp = kp2;
+        vp = vp2;
+        pg = pg2;
+        pg2 = pg3;
+      }
+    }
+
+    if (!ok && lane == 0 && !*abort_flag) fail();
+  } else {
+    regs_lower<kRegsIssue>();
+    if (warp == 12 && lane == 0) {
+      // ================================================================ products
+      const uint64_t q0 = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024);
+      const uint64_t k0 = smem_desc(smem_u32(smem + C::kOffK), 16, 1024);
+      const uint64_t v0 = smem_desc(smem_u32(smem + C::kOffV), 128 * 128, 1024);
+      int n = 0, item = 0, pc[2] = {0, 0}, qc[2] = {0, 0};
+      bool ok = true;
+      // S of query tile x and token tile t
+      auto issue_s = [&](int x, int t) {
+        const uint64_t a = q0 + (uint64_t)(x * (C::kTileBytes >> 4));
+        const uint64_t b = k0 + (uint64_t)((t & 1) * (C::kTileBytes >> 4));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t at = (uint64_t)(((k / 4) * (128 * 128) + (k % 4) * 32) >> 4);
+          umma_f16_ss(tmem + x * 128, a + at, b + at, C::kDescS, k > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int x, int t, bool first) {
+        const uint64_t b = v0 + (uint64_t)((t & 1) * (C::kTileBytes >> 4));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma_f16_ts(tmem + C::kTmO + x * D, tmem + x * 128 + k * 8, b + (uint64_t)(k * 128), C::kDescO,
+                      k > 0 || !first ? 1u : 0u);
+      };
+      for (; w.more() && ok; w.next(p), ++item) {
+        const int begin = w.begin(), end = w.end();
+        const int tiles = item_rows() > 128 ? 2 : 1;
+        for (int j = begin; ok && j <= end; ++j) {
+          // for each query tile: PV(j - 1), then S(j); token tile j is number n
+          for (int x = 0; ok && x < 2; ++x) {
+            if (j > begin) {
+              ok = wait(&p_full[x], pc[x] & 1);
+              ++pc[x];
+              if (ok && x == 0) ok = wait(&v_full[(n - 1) & 1], ((n - 1) >> 1) & 1);
+              if (!ok) break;
+            }
+            if (x < tiles) {
+              tc_fence_after();
+              if (j > begin) issue_pv(x, n - 1, j - 1 == begin);
+              if (j < end) {
+                if (j == begin) {
+                  ok = wait(&q_full[x], qc[x] & 1);
+                  ++qc[x];
+                }
+                if (ok && x == 0) ok = wait(&k_full[n & 1], (n >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(x, n);
+              }
+            }
+            // tile B's barriers tell when buffers are free, with or without a tile B
+            umma_commit(j < end ? &s_bar[x * 2 + (n & 1)] : &o_bar[x * 2 + (item & 1)]);
+          }
+          if (j < end) ++n;
+        }
+      }
+      if (!ok) {
+        if (!*abort_flag) fail();
+      }
+      // nothing in flight when TMEM goes
+      umma_commit(drain);
+      volatile int never = 0;
+      mbar_wait_bounded(drain, 0, &never, kTimeoutNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int launch(const SplitParams& p, cudaStream_t stream) {
+  using C = MC<D>;
+  auto kern = kv4_many_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+    return SBSA_ERR_CUDA;
+  const int grid = split_grid();
+  if (grid <= 0) return SBSA_ERR_CUDA;
+  kern<<<grid, kThreads, C::kSmem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return SBSA_ERR_CUDA;
+  return launch_join<D, kRows, kRows, true, __nv_bfloat16>(p, grid, stream);
+}
+
+}  // namespace
+
+size_t kv4_many_workspace(int d) { return split_workspace(kRows, d); }
+
+int launch_kv4_many(const Kv4AttendArgs& a, cudaStream_t stream) {
+  const SplitParams p = split_params(a, kRows);
+  return a.d == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+}
+
+}  // namespace sbsa

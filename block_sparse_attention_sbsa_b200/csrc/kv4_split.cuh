@@ -1,0 +1,305 @@
+// How attention over the 4-bit cache is shared out over the CTAs, and how the
+// parts of what several CTAs share are joined.
+//
+// The rows of one kv head (or listed query head) of a sequence, in tiles of
+// ROWS, are items; an item's tokens fall into units of 128.  Item after item,
+// each costs COST (rows, joining, output) and then one for each unit; the whole is
+// cut into equal runs, one for each CTA, so that ragged batches and single long
+// contexts both fill the GPU.  Each CTA finds its run by a scan over the items'
+// sizes: nothing is read by the host, and the cuts depend on the sizes alone.
+#pragma once
+#include <cfloat>
+
+#include "kv4.cuh"
+#include "tma_map.h"
+
+namespace sbsa {
+namespace {
+
+constexpr int kSplitUnit = 128;
+constexpr int kMaxCtas = 160;
+
+struct Part {  // the item whose first part a CTA holds, and its number of parts (0: none)
+  int parts, seq, head, tile;
+};
+
+// A slot holds the partial rows of one item: [rows][d] outputs, their references
+// and their weights' sums.
+constexpr size_t slot_floats(int rows, int d) { return (size_t)rows * (d + 2); }
+
+inline size_t split_workspace(int rows, int d) {
+  return kMaxCtas * (2 * slot_floats(rows, d) * sizeof(float) + sizeof(Part));
+}
+
+struct SplitParams {
+  Kv4AttendArgs a;
+  int heads;         // items per sequence and row tile: kv heads, or listed query heads
+  int group;         // query heads of an item
+  int kv_div;        // item head / kv_div = kv head
+  float scale_log2;  // sm_scale * log2(e)
+  float* slots;      // two a CTA: of the item that begins before its run, and of the one that
+                     // goes on behind it
+  Part* parts;       // one a CTA
+};
+
+inline SplitParams split_params(const Kv4AttendArgs& a, int slot_rows) {
+  SplitParams p{};
+  p.a = a;
+  p.heads = a.list_heads ? a.list_heads : a.b.hkv;
+  p.group = a.hq / p.heads;
+  p.kv_div = p.heads / a.b.hkv;
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.slots = static_cast<float*>(a.workspace);
+  p.parts = reinterpret_cast<Part*>(p.slots + kMaxCtas * 2 * slot_floats(slot_rows, a.d));
+  return p;
+}
+
+inline int split_grid() {
+  const int n = sm_count();
+  return n < kMaxCtas ? n : kMaxCtas;
+}
+
+// A sequence as an item sees it.
+struct Seq {
+  int first, rows, len;  // first row, number of rows, tokens
+};
+
+__device__ __forceinline__ Seq seq_of(const SplitParams& p, int b) {
+  Seq s;
+  const int lo = clamp_int(p.a.b.cu[b], 0, p.a.b.n_tokens);
+  const int hi = clamp_int(p.a.b.cu[b + 1], lo, p.a.b.n_tokens);
+  s.first = lo;
+  s.rows = hi - lo;
+  s.len = kv4_len(p.a.b, b);
+  return s;
+}
+
+// Row `row` of the item head: the token row, its number in the sequence and the
+// query head; false past the last.
+__device__ __forceinline__ bool row_of(const SplitParams& p, const Seq& s, int head, long long row,
+                                       long long* t, int* h, int* i) {
+  *i = (int)(row / p.group);
+  if (*i >= s.rows) return false;
+  *t = s.first + *i;
+  *h = head * p.group + (int)(row % p.group);
+  return true;
+}
+
+// The items of one (sequence, head).
+template <int ROWS>
+struct Items {
+  Seq seq;
+  int tiles;
+  int listed;  // units of the listed blocks, -1 without lists
+
+  __device__ Items() {}
+  __device__ Items(const SplitParams& p, int b, int head) {
+    seq = seq_of(p, b);
+    tiles = (int)(((long long)seq.rows * p.group + ROWS - 1) / ROWS);
+    listed = -1;
+    if (p.a.list_heads) {
+      const int n = clamp_int(p.a.cnt[(long long)b * p.heads + head], 0, p.a.max_blocks);
+      listed = (n * p.a.block + kSplitUnit - 1) / kSplitUnit;
+    }
+  }
+  // Tokens that the tile's last row sees.
+  __device__ int limit(const SplitParams& p, int tile) const {
+    const long long rows = min((long long)(tile + 1) * ROWS, (long long)seq.rows * p.group);
+    return max(0, seq.len - seq.rows + (int)((rows - 1) / p.group) + 1);
+  }
+  // Units of a tile; one that sees nothing still takes one (it writes zeros).
+  __device__ int units(const SplitParams& p, int tile) const {
+    const int n = listed >= 0 ? listed : (limit(p, tile) + kSplitUnit - 1) / kSplitUnit;
+    return n < 1 ? 1 : n;
+  }
+  template <int COST>
+  __device__ long long cost(const SplitParams& p) const {
+    long long c = (long long)tiles * COST;
+    for (int i = 0; i < tiles; ++i) c += units(p, i);
+    return c;
+  }
+};
+
+// A CTA's run: where it begins, and the cut of the whole.
+struct Run {
+  int b, head, tile, cost;  // first item, and how much of its cost lies before the run
+  int ctas;
+  long long total, begin, end;
+};
+
+template <int THREADS>
+constexpr int kScanBytes = (THREADS / 32 + 2) * 8 + 16;
+
+// All threads of the CTA together, with kScanBytes of shared memory; false when
+// the CTA has no run.  Ends with the CTA in step (earlier writes to shared memory are
+// visible).  Also clears the CTA's entry of p.parts, and lets the joining kernel start up.
+template <int ROWS, int COST, int THREADS>
+__device__ __forceinline__ bool split_run(const SplitParams& p, long long* s_scan, Run* run) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* s_start = reinterpret_cast<int*>(s_scan + THREADS / 32);
+  const int items = p.a.b.n_seqs * p.heads;
+  const int per = (items + THREADS - 1) / THREADS;
+  const int i0 = min(items, (int)threadIdx.x * per), i1 = min(items, i0 + per);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i)
+    mine += Items<ROWS>(p, i / p.heads, i % p.heads).template cost<COST>(p);
+  long long incl = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+    if (lane >= m) incl += x;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) p.parts[cta].parts = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (cta >= ctas) return false;
+  run->ctas = ctas;
+  run->total = total;
+  run->begin = total * cta / ctas;
+  run->end = total * (cta + 1) / ctas;
+  if (run->begin >= before && run->begin < before + mine) {
+    long long x = run->begin - before;
+    for (int i = i0; i < i1; ++i) {
+      const Items<ROWS> it(p, i / p.heads, i % p.heads);
+      int t = 0;
+      for (; t < it.tiles; ++t) {
+        const long long c = COST + it.units(p, t);
+        if (x < c) break;
+        x -= c;
+      }
+      if (t < it.tiles) {
+        s_start[0] = i / p.heads;
+        s_start[1] = i % p.heads;
+        s_start[2] = t;
+        s_start[3] = (int)x;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  run->b = s_start[0], run->head = s_start[1], run->tile = s_start[2], run->cost = s_start[3];
+  return true;
+}
+
+// Walks the items of a run.  Units [begin, end) of the current item are the
+// CTA's; a run that ends within an item's COST leaves it to the next CTA.
+template <int ROWS, int COST>
+struct SplitWalk : Items<ROWS> {
+  int b, head, tile, unit_count;
+  int item_limit;
+  long long before, left;  // cost from the item's start to the run's begin and end
+
+  __device__ SplitWalk(const SplitParams& p, const Run& r) : Items<ROWS>(p, r.b, r.head) {
+    b = r.b, head = r.head, tile = r.tile;
+    before = r.cost;
+    left = r.cost + r.end - r.begin;
+    set(p);
+  }
+  __device__ void set(const SplitParams& p) {
+    unit_count = this->units(p, tile);
+    item_limit = Items<ROWS>::limit(p, tile);
+  }
+  __device__ int limit() const { return item_limit; }
+  __device__ int begin() const { return before > COST ? (int)before - COST : 0; }
+  __device__ int end() const {
+    const long long e = left - COST;
+    return e < 0 ? 0 : e < unit_count ? (int)e : unit_count;
+  }
+  __device__ bool whole() const { return begin() == 0 && end() == unit_count; }
+  __device__ bool more() const { return left > COST; }
+  __device__ void next(const SplitParams& p) {
+    left -= COST + unit_count;
+    before = 0;
+    if (left <= COST) return;
+    if (++tile == this->tiles) {
+      tile = 0;
+      do {
+        if (++head == p.heads) {
+          head = 0;
+          if (++b == p.a.b.n_seqs) {
+            left = 0;
+            return;
+          }
+        }
+        static_cast<Items<ROWS>&>(*this) = Items<ROWS>(p, b, head);
+      } while (this->tiles == 0);
+    }
+    set(p);
+  }
+  // The CTA's entry of p.parts for an item that begins here and goes on in the next
+  // CTAs, up to the one that owns its last unit.
+  __device__ Part part(const Run& r, int cta) const {
+    const long long last = r.end - left + COST + unit_count - 1;
+    const int owner = (int)(((last + 1) * r.ctas + r.total - 1) / r.total) - 1;
+    return Part{owner - cta + 1, b, head, tile};
+  }
+};
+
+// Joins the parts of the item that begins in CTA blockIdx.x and goes on in the next
+// ones; a CTA takes every gridDim.y-th row, a thread one place of the slots' rows (channel
+// `place` itself, or as kPermuted says, see kv4_many.cu).
+template <int D, int ROWS, int SLOT_ROWS, bool kPermuted, typename T>
+__global__ void __launch_bounds__(D) kv4_join_kernel(const __grid_constant__ SplitParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Part part = p.parts[blockIdx.x];
+  if (part.parts < 2) return;
+  const Seq s = seq_of(p, part.seq);
+  const int c = threadIdx.x;
+  int channel = c;
+  if (kPermuted)
+    channel = D == 128 ? 32 * (2 * ((c >> 3) & 1) + (c & 1)) + 4 * (c >> 4) + ((c & 7) >> 1)
+                       : 32 * (c & 1) + 4 * (c >> 3) + ((c & 7) >> 1);
+  auto slot = [&](int k) {
+    return p.slots + (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) *
+                         slot_floats(SLOT_ROWS, D);
+  };
+  for (int row = blockIdx.y; row < ROWS; row += gridDim.y) {
+    long long t;
+    int h, i;
+    if (!row_of(p, s, part.head, (long long)part.tile * ROWS + row, &t, &h, &i)) return;
+    float top = -FLT_MAX;
+    for (int k = 0; k < part.parts; ++k) top = fmaxf(top, slot(k)[SLOT_ROWS * D + row]);
+    float acc = 0.f, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < part.parts; ++k) {
+      const float* x = slot(k);
+      const float fac = exp2f(x[SLOT_ROWS * D + row] - top);
+      sum = fmaf(fac, x[SLOT_ROWS * (D + 1) + row], sum);
+      acc = fmaf(fac, x[row * D + c], acc);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T* dst = static_cast<T*>(p.a.o) + t * p.a.o_token + h * p.a.o_head + channel;
+    if constexpr (sizeof(T) == 4)
+      *dst = acc * inv;
+    else
+      *dst = __float2bfloat16(acc * inv);
+  }
+}
+
+// Behind the attending kernel, which lets it start up early.
+template <int D, int ROWS, int SLOT_ROWS, bool kPermuted, typename T>
+int launch_join(const SplitParams& p, int grid, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, ROWS < 16 ? ROWS : 16);
+  cfg.blockDim = dim3(D);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, ROWS, SLOT_ROWS, kPermuted, T>, p) == cudaSuccess
+             ? SBSA_OK
+             : SBSA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace sbsa

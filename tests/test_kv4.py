@@ -351,6 +351,23 @@ def test_attend_chunks(kv4, cuda, hq, hkv, d, page, dtype, new):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,most", [(64, 1), (128, 5), (64, 150), (128, 90)])
+def test_attend_many_items_a_cta(kv4, cuda, d, most):
+    """Enough sequences of mixed sizes that every CTA walks several items, whole and shared, with one
+    and two query tiles, of one and many token tiles, in mixed order."""
+    rng = np.random.default_rng(most)
+    seqs = 160 if most < 9 else 36
+    lens = [int(x) for x in np.exp(rng.uniform(np.log(3), np.log(1500 if most < 9 else 2500), seqs))]
+    new = [min(n, int(rng.integers(0, most + 1)) if rng.random() < 0.5 else most) for n in lens]
+    b = _fast_fill(Batch(lens, new, 64, 2, d, seed=most), rng).gpu()
+    q = _rows(rng, 8, b.total, d, "bf16", True, 1.5)
+    out = torch.zeros_like(q)
+    kv4.attend(b.g_cache, q, *b.g, max(new), out=out)
+    assert _status(kv4) == 0
+    _check(kv4, b, q, out, torch.zeros_like(out))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("list_heads", ["kv", "q"])
 @pytest.mark.parametrize("block,page,d,dtype", [(64, 64, 128, "bf16"), (128, 16, 64, "fp32"), (128, 128, 128, "bf16"),
                                                 (64, 32, 64, "bf16")])
