@@ -728,11 +728,9 @@ template <int D, int NT, typename T>
 int launch(const SplitParams& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   auto kern = kv4_attend_kernel<D, NT, T>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-    return SBSA_ERR_CUDA;
-  int grid = sm_count();
+  static SplitGrid ctas;
+  const int grid = ctas.get(reinterpret_cast<const void*>(kern), C::kSmem);
   if (grid <= 0) return SBSA_ERR_CUDA;
-  grid = grid < kMaxCtas ? grid : kMaxCtas;
   kern<<<grid, kThreads, C::kSmem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SBSA_ERR_CUDA;
   return launch_join<D, 8 * NT, kSlotRows, false, T>(p, grid, stream);

@@ -620,9 +620,8 @@ template <int D>
 int launch(const SplitParams& p, cudaStream_t stream) {
   using C = MC<D>;
   auto kern = kv4_many_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-    return SBSA_ERR_CUDA;
-  const int grid = split_grid();
+  static SplitGrid ctas;
+  const int grid = ctas.get(reinterpret_cast<const void*>(kern), C::kSmem);
   if (grid <= 0) return SBSA_ERR_CUDA;
   kern<<<grid, kThreads, C::kSmem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SBSA_ERR_CUDA;

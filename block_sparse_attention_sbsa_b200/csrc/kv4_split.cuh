@@ -8,6 +8,7 @@
 // contexts both fill the GPU.  Each CTA finds its run by a scan over the items'
 // sizes: nothing is read by the host, and the cuts depend on the sizes alone.
 #pragma once
+#include <atomic>
 #include <cfloat>
 
 #include "kv4.cuh"
@@ -54,9 +55,29 @@ inline SplitParams split_params(const Kv4AttendArgs& a, int slot_rows) {
   return p;
 }
 
-inline int split_grid() {
-  const int n = sm_count();
-  return n < kMaxCtas ? n : kMaxCtas;
+// What a launch has to know of the current device, asked once a device and kernel (the
+// questions cost as much as a launch): the CTAs of the grid, 0 on an error.
+struct SplitGrid {
+  std::atomic<int> ctas[64] = {};
+  int get(const void* kernel, int smem_bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = ctas[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) !=
+        cudaSuccess)
+      return 0;
+    n = sm_count();
+    n = n < kMaxCtas ? n : kMaxCtas;
+    ctas[dev].store(n, std::memory_order_relaxed);
+    return n;
+  }
+};
+
+// Whether an item can have more than one unit, and so more than one CTA.
+inline bool split_possible(const Kv4AttendArgs& a) {
+  if (a.list_heads) return (long long)a.max_blocks * a.block > kSplitUnit;
+  return (long long)a.b.max_pages * a.b.page > kSplitUnit;
 }
 
 // A sequence as an item sees it.
@@ -287,6 +308,7 @@ __global__ void __launch_bounds__(D) kv4_join_kernel(const __grid_constant__ Spl
 // Behind the attending kernel, which lets it start up early.
 template <int D, int ROWS, int SLOT_ROWS, bool kPermuted, typename T>
 int launch_join(const SplitParams& p, int grid, cudaStream_t stream) {
+  if (!split_possible(p.a)) return SBSA_OK;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

@@ -51,6 +51,8 @@ lib.sbsa_kv4_attend.argtypes = [_PP, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _
                                 _vp, _vp, ctypes.c_size_t, _vp]
 lib.sbsa_kv4_attend.restype = ctypes.c_int
 
+_append, _read, _attend = lib.sbsa_kv4_append, lib.sbsa_kv4_read, lib.sbsa_kv4_attend
+
 _DTYPE = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
@@ -65,15 +67,11 @@ def empty(n_pages: int, n_kv_heads: int, page_size: int = 64, head_dim: int = 12
                        device=device)
 
 
-def _on(t: torch.Tensor, name: str, device):
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+# The calls are short (a few microseconds on the GPU for a token), so the checks that every call
+# passes are single expressions; what fails one is looked at again to say what is wrong.
 
-
-def _batch(cache, page_table, seq_lens, cu_new) -> Params:
-    """The parameters that every call has, from checked tensors."""
-    dev = cache.device
-    if dev.type != "cuda":
+def _bad_batch(cache, page_table, seq_lens, cu_new):
+    if not cache.is_cuda:
         raise ValueError("cache must be a CUDA tensor")
     if cache.dtype != torch.uint8 or cache.dim() != 5 or cache.shape[2] != 2 \
             or cache.shape[4] % 5 or not cache.is_contiguous():
@@ -82,126 +80,152 @@ def _batch(cache, page_table, seq_lens, cu_new) -> Params:
     n_seqs = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
     for t, name, shape in ((page_table, "page_table", (n_seqs, page_table.shape[-1])),
                            (seq_lens, "seq_lens", (n_seqs,)), (cu_new, "cu_new", (n_seqs + 1,))):
-        _on(t, name, dev)
-        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}, "
-                             f"got {t.dtype} {tuple(t.shape)}")
-    return Params(n_q_heads=cache.shape[1], n_kv_heads=cache.shape[1],
-                  head_dim=cache.shape[4] // 5 * 8, page_size=cache.shape[3],
-                  n_pages=cache.shape[0], max_pages=page_table.shape[1], n_seqs=n_seqs, max_new=1)
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() \
+                or t.device != cache.device:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on "
+                             f"{cache.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    raise ValueError("inconsistent cache, page_table, seq_lens and cu_new")
 
 
-def _rows(p: Params, t: torch.Tensor, name: str, heads: int, dtype, device):
-    """Pointer and strides of rows [heads, n_tokens, d]."""
-    _on(t, name, device)
-    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != heads or t.shape[1] != p.n_tokens \
-            or t.shape[2] != p.head_dim:
-        raise ValueError(f"{name} must be {dtype} {(heads, p.n_tokens, p.head_dim)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if t.stride(2) != 1 and t.numel():
-        raise ValueError(f"{name} must have contiguous channels")
-    return t.data_ptr(), t.stride(1), t.stride(0)
+_U8, _I32 = torch.uint8, torch.int32
 
 
-def _plain(p: Params, t: Optional[torch.Tensor], name: str, dtype, device):
+def _batch(cache, page_table, seq_lens, cu_new):
+    """Device index, shape of the cache, and of the page table, checked."""
+    dev, shape, tab, lens = cache.get_device(), cache.shape, page_table.shape, seq_lens.shape
+    if (dev < 0 or len(shape) != 5 or shape[2] != 2 or shape[4] % 5 or cache.dtype is not _U8
+            or len(tab) != 2 or len(lens) != 1 or tab[0] != lens[0]
+            or cu_new.shape != (lens[0] + 1,)
+            or page_table.dtype is not _I32 or seq_lens.dtype is not _I32
+            or cu_new.dtype is not _I32 or page_table.get_device() != dev
+            or seq_lens.get_device() != dev or cu_new.get_device() != dev
+            or not (cache.is_contiguous() and page_table.is_contiguous()
+                    and seq_lens.is_contiguous() and cu_new.is_contiguous())):
+        _bad_batch(cache, page_table, seq_lens, cu_new)
+    return dev, shape, tab
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype, dev: int):
+    """Strides between tokens and heads of rows [heads, n_tokens, d]."""
+    head, token, channel = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.shape != shape or t.dtype is not dtype or channel != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} with contiguous channels on "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} "
+                         f"on {t.device}")
+    return token, head
+
+
+def _plain(t: Optional[torch.Tensor], name: str, shape, dtype, dev: int):
     """Pointer of a contiguous [Hkv, n_tokens, d] tensor, or None."""
     if t is None:
         return None
-    _rows(p, t, name, p.n_kv_heads, dtype, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on cuda:{dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _DTYPE:
-        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    return _DTYPE[t.dtype]
+    code = _DTYPE.get(t.dtype)
+    if code is None or t.dim() != 3:
+        raise ValueError(f"{name} must be a bfloat16 or float32 tensor [heads, tokens, d], got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    return code
 
 
-def _call(fn, name: str, device, stream, *args):
+def _call(fn, name: str, dev: int, stream, *args):
     """The C call with the tensors' device current."""
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, s), name)
+    s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    if dev == torch.cuda.current_device():
+        code = fn(*args, s)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, s), name)
+        with torch.cuda.device(dev):
+            code = fn(*args, s)
+    if code:
+        _check(code, name)
 
 
 def append(cache, k, v, page_table, seq_lens, cu_new, k_stored=None, v_stored=None, stream=None):
     """Quantise the new rows k, v [Hkv, n_tokens, d] into the cache.  With k_stored / v_stored
     (contiguous, like k and v) also what the cache now stands for."""
-    p, dev = _batch(cache, page_table, seq_lens, cu_new), cache.device
-    p.dtype = _dtype(k, "k")
-    p.n_tokens = k.shape[1] if k.dim() == 3 else -1
-    kr = _rows(p, k, "k", p.n_kv_heads, k.dtype, dev)
-    vr = _rows(p, v, "v", p.n_kv_heads, k.dtype, dev)
-    _call(lib.sbsa_kv4_append, "sbsa_kv4_append", dev, stream, ctypes.byref(p), cache.data_ptr(),
-          page_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(), *kr, *vr,
-          _plain(p, k_stored, "k_stored", k.dtype, dev), _plain(p, v_stored, "v_stored", k.dtype, dev))
+    dev, c, tab = _batch(cache, page_table, seq_lens, cu_new)
+    dt, code = k.dtype, _dtype(k, "k")
+    heads, d, n = c[1], c[4] // 5 * 8, k.shape[1]
+    shape = (heads, n, d)
+    kr, vr = _rows(k, "k", shape, dt, dev), _rows(v, "v", shape, dt, dev)
+    p = Params(heads, heads, d, c[3], c[0], tab[1], tab[0], n, 1, code)
+    _call(_append, "sbsa_kv4_append", dev, stream, p, cache.data_ptr(), page_table.data_ptr(),
+          seq_lens.data_ptr(), cu_new.data_ptr(), k.data_ptr(), *kr, v.data_ptr(), *vr,
+          _plain(k_stored, "k_stored", shape, dt, dev),
+          _plain(v_stored, "v_stored", shape, dt, dev))
 
 
 def read(cache, page_table, seq_lens, cu_new, k_out=None, v_out=None, stream=None):
     """The same rows back into k_out and / or v_out [Hkv, n_tokens, d] (contiguous, bf16 or fp32).
     With cu_new the running sum of seq_lens: whole sequences."""
-    p, dev = _batch(cache, page_table, seq_lens, cu_new), cache.device
-    some = k_out if k_out is not None else v_out
+    dev, c, tab = _batch(cache, page_table, seq_lens, cu_new)
+    some = v_out if k_out is None else k_out
     if some is None:
         raise ValueError("read needs k_out or v_out")
-    p.dtype = _dtype(some, "k_out" if k_out is not None else "v_out")
-    p.n_tokens = some.shape[1] if some.dim() == 3 else -1
-    _call(lib.sbsa_kv4_read, "sbsa_kv4_read", dev, stream, ctypes.byref(p), cache.data_ptr(),
-          page_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(),
-          _plain(p, k_out, "k_out", some.dtype, dev), _plain(p, v_out, "v_out", some.dtype, dev))
+    dt, code = some.dtype, _dtype(some, "k_out or v_out")
+    heads, d, n = c[1], c[4] // 5 * 8, some.shape[1]
+    shape = (heads, n, d)
+    p = Params(heads, heads, d, c[3], c[0], tab[1], tab[0], n, 1, code)
+    _call(_read, "sbsa_kv4_read", dev, stream, p, cache.data_ptr(), page_table.data_ptr(),
+          seq_lens.data_ptr(), cu_new.data_ptr(), _plain(k_out, "k_out", shape, dt, dev),
+          _plain(v_out, "v_out", shape, dt, dev))
 
 
 def attend(cache, q, page_table, seq_lens, cu_new, max_new: int, idx=None, cnt=None,
            block_size: int = 0, sm_scale: float = 0.0, out=None, workspace=None, stream=None):
     """o [Hq, n_tokens, d] (into `out` when given) of causal attention of the rows q over the
-    cache, which holds their own tokens already.  max_new: at least the most rows of one sequence.  idx [n_seqs, heads,
-    max_blocks] and cnt [n_seqs, heads] (heads = Hkv or Hq) restrict it to the listed blocks of
-    block_size tokens.  workspace: uint8, at least attend_workspace_bytes (allocated when None)."""
-    p, dev = _batch(cache, page_table, seq_lens, cu_new), cache.device
-    p.dtype = _dtype(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [Hq, n_tokens, d]")
-    p.n_q_heads, p.n_tokens, p.max_new, p.sm_scale = q.shape[0], q.shape[1], max_new, sm_scale
+    cache, which holds their own tokens already.  max_new: at least the most rows of one sequence.
+    idx [n_seqs, heads, max_blocks] and cnt [n_seqs, heads] (heads = Hkv or Hq) restrict it to the
+    listed blocks of block_size tokens.  workspace: uint8, at least attend_workspace_bytes
+    (allocated when None)."""
+    dev, c, tab = _batch(cache, page_table, seq_lens, cu_new)
+    dt, code = q.dtype, _dtype(q, "q")
+    heads, n, d = q.shape[0], q.shape[1], c[4] // 5 * 8
+    shape = (heads, n, d)
+    qr = _rows(q, "q", shape, dt, dev)
     if out is None:
         with torch.cuda.stream(stream):
             out = torch.zeros_like(q)
-    qr = _rows(p, q, "q", p.n_q_heads, q.dtype, dev)
-    orow = _rows(p, out, "out", p.n_q_heads, q.dtype, dev)
-    if (idx is None) != (cnt is None):
-        raise ValueError("idx and cnt go together")
-    if idx is not None:
-        if idx.dim() != 3 or idx.dtype != torch.int32 or not idx.is_contiguous() \
-                or idx.shape[0] != p.n_seqs or idx.shape[1] not in (p.n_kv_heads, p.n_q_heads):
-            raise ValueError("idx must be contiguous int32 [n_seqs, Hkv or Hq, max_blocks]")
-        if cnt.dtype != torch.int32 or not cnt.is_contiguous() \
-                or tuple(cnt.shape) != tuple(idx.shape[:2]):
-            raise ValueError(f"cnt must be contiguous int32 {tuple(idx.shape[:2])}")
-        _on(idx, "idx", dev)
-        _on(cnt, "cnt", dev)
+    orow = _rows(out, "out", shape, dt, dev)
+    p = Params(heads, c[1], d, c[3], c[0], tab[1], tab[0], n, max_new, code, 0, 0, 0, sm_scale)
+    lists = (None, None)
+    if idx is not None or cnt is not None:
+        if idx is None or cnt is None:
+            raise ValueError("idx and cnt go together")
+        if idx.dim() != 3 or idx.dtype is not _I32 or not idx.is_contiguous() \
+                or idx.shape[0] != tab[0] or idx.shape[1] not in (c[1], heads) \
+                or idx.get_device() != dev:
+            raise ValueError("idx must be contiguous int32 [n_seqs, Hkv or Hq, max_blocks] on "
+                             f"cuda:{dev}")
+        if cnt.dtype is not _I32 or not cnt.is_contiguous() or cnt.shape != idx.shape[:2] \
+                or cnt.get_device() != dev:
+            raise ValueError(f"cnt must be contiguous int32 {tuple(idx.shape[:2])} on cuda:{dev}")
         p.list_heads, p.max_blocks, p.block_size = idx.shape[1], idx.shape[2], block_size
+        lists = (idx.data_ptr(), cnt.data_ptr())
     if workspace is None:
-        # with the call's stream current, so that the memory is not given away before it has run
-        with torch.cuda.stream(stream):
-            workspace = torch.empty(attend_workspace_bytes(p), dtype=torch.uint8, device=dev)
-    else:
-        _on(workspace, "workspace", dev)
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor")
-    _call(lib.sbsa_kv4_attend, "sbsa_kv4_attend", dev, stream, ctypes.byref(p), cache.data_ptr(),
-          page_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(), *qr, *orow,
-          None if idx is None else idx.data_ptr(), None if cnt is None else cnt.data_ptr(),
+        size = attend_workspace_bytes(p)
+        if stream is None:
+            workspace = torch.empty(size, dtype=_U8, device=cache.device)
+        else:  # with the call's stream current: the memory is not given away before it has run
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(size, dtype=_U8, device=cache.device)
+    elif workspace.dtype is not _U8 or not workspace.is_contiguous() \
+            or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
+    _call(_attend, "sbsa_kv4_attend", dev, stream, p, cache.data_ptr(), page_table.data_ptr(),
+          seq_lens.data_ptr(), cu_new.data_ptr(), q.data_ptr(), *qr, out.data_ptr(), *orow, *lists,
           workspace.data_ptr(), workspace.numel())
     return out
 
 
 def attend_workspace_bytes(p: Params) -> int:
-    """Bytes of the workspace of `attend` (the same for every batch of one head_dim)."""
-    n = lib.sbsa_kv4_attend_workspace_bytes(ctypes.byref(p))
+    """Bytes of the workspace of `attend`."""
+    n = lib.sbsa_kv4_attend_workspace_bytes(p)
     if n == 0:
         raise SbsaError(ERR_INVALID_ARG, "sbsa_kv4_attend_workspace_bytes")
-    return int(n)
+    return n
