@@ -20,13 +20,14 @@
 //             back over its first half; the reference maximum moves (and O is
 //             rescaled in TMEM) only when it is outgrown by 2^8.  They write their
 //             tile's Q into shared memory and O to global memory.
-//   8-11      a thread has a token of the tile: reads its levels from global memory
-//             one tile ahead and writes its K and V rows into the swizzled layout of
-//             the products' operands (two buffers each; the channels in the order in
+//   8-11      a thread has a token of the tile: takes its levels from a ring of three
+//             half tiles (keys or values) and writes its K and V rows into the swizzled layout
+//             of the products' operands (two buffers each; the channels in the order in
 //             which they come out of the words, which Q and the output follow).
 //   12        issues the products: [PV_A(j-1), S_A(j)], [PV_B(j-1), S_B(j)], ...; one
 //             commit each announces S, that the O of the tile is at rest, and (B's) that
 //             K(j) and V(j-1) are free again.
+//   13        copies whole pages into the ring (bulk copies).
 // The items and their cut over the CTAs: kv4_split.cuh.  Every wait is bounded (2 s).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -45,9 +46,11 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kRows = 256;  // of an item: two tiles of 128
 constexpr int kItemCost = 2;
 constexpr int kThreads = 512;
-// 256 * 184 + 128 * 96 + 128 * 48 = 512 * 128, what the block is launched with
-constexpr int kRegsSoftmax = 184, kRegsUnpack = 96, kRegsIssue = 48;
+// 256 * 184 + 128 * 80 + 128 * 64 = 512 * 128, what the block is launched with
+constexpr int kRegsSoftmax = 184, kRegsUnpack = 80, kRegsIssue = 64;
 constexpr float kRescaleLog2 = 8.0f;
+
+constexpr int kHalves = 3;
 
 template <int D>
 struct MC {
@@ -56,14 +59,17 @@ struct MC {
   static constexpr int kOffQ = 0;                  // Q[2]
   static constexpr int kOffK = 2 * kTileBytes;     // K[2]
   static constexpr int kOffV = 4 * kTileBytes;     // V[2]
-  static constexpr int kOffInfo = 6 * kTileBytes;  // Info[4]
+  static constexpr int kHalfBytes = 128 * (D / 8) * 5;  // levels and pairs of 128 keys (or values)
+  static constexpr int kOffRing = 6 * kTileBytes;       // [kHalves]
+  static constexpr int kOffInfo = kOffRing + kHalves * kHalfBytes;  // Info[4]
   static constexpr int kInfoBytes = 32;
   static constexpr int kOffNan = kOffInfo + 4 * kInfoBytes;  // int[4 items][4 groups]
   static constexpr int kOffMax = kOffNan + 64;               // uint32[2 parities][4 warps][2]
-  static constexpr int kOffScan = kOffMax + 64;
+  static constexpr int kOffPages = kOffMax + 64;             // int[kHalves][8]: the pages' numbers
+  static constexpr int kOffScan = kOffPages + kHalves * 32;
   static constexpr int kOffBar = kOffScan + kScanBytes<kThreads>;
-  // q_full[2] k_full[2] v_full[2] s_bar[2][2] o_bar[2][2] p_full[2] drain
-  static constexpr int kBars = 2 + 2 + 2 + 4 + 4 + 2 + 1;
+  // q_full[2] k_full[2] v_full[2] s_bar[2][2] o_bar[2][2] p_full[2] drain c_full[3] c_free[3]
+  static constexpr int kBars = 2 + 2 + 2 + 4 + 4 + 2 + 1 + 2 * kHalves;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static constexpr uint32_t kDescS = make_idesc(0, 128, 128, false, false);
@@ -116,6 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
   uint64_t* o_bar = bar + 10;      // [tile * 2 + (item & 1)]: the item's last PV done
   uint64_t* p_full = bar + 14;     // [tile]
   uint64_t* drain = bar + 16;
+  uint64_t* c_full = bar + 17;     // [half tile % kHalves]
+  uint64_t* c_free = c_full + kHalves;
+  int* s_pages = reinterpret_cast<int*>(smem + C::kOffPages);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   Info* info = reinterpret_cast<Info*>(smem + C::kOffInfo);
@@ -133,6 +142,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_bar[i], 1);
       mbar_init(&o_bar[i], 1);
+    }
+    for (int i = 0; i < kHalves; ++i) {
+      mbar_init(&c_full[i], 1);
+      mbar_init(&c_free[i], 128);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -375,60 +388,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     const int tok = threadIdx.x - 256;
     const int page = p.a.b.page, page_log = __ffs(page) - 1, rec = kv4_rec_bytes(page, D);
     constexpr int kWords = D / 32;  // 16-byte pieces of a row of levels
+    const int off = tok & (page - 1);
+    const int turn = NG == 4 ? ((off >> 1) & 1) * 2 : 0;  // pieces of a value's row change places
+    // with 4 pieces, neighbouring pairs of tokens begin at different ones: no bank is met twice
+    const int first = NG == 4 ? (tok >> 1) & 3 : 0;
+    const unsigned char* ring = smem + C::kOffRing + (tok >> page_log) * rec;
     int n = 0, item = 0;
-
     int ended[2] = {0, 0};  // by buffer: 1 + the item that ended with its last token tile, else 0
+    int kh = 0, kph = 0;    // ring place and phase of the keys of tile n; the values' follow them
     bool ok = true;
     for (; w.more() && ok; w.next(p), ++item) {
-      const int begin = w.begin(), end = w.end(), limit = w.limit();
-      const int32_t* table = p.a.b.table + (long long)w.b * p.a.b.max_pages;
-      const uint8_t* heads = p.a.cache + (long long)w.head * 2 * rec;
-      // this thread's token of token tile j: its page number, -1 behind the last token, -2 where the
-      // page is not in the cache
-      auto look = [&](int j) {
-        const int pos = j * 128 + tok;
-        if (j >= end || pos >= limit) return -1;
-        const int pg = table[pos >> page_log];
-        return pg < 0 || pg >= p.a.b.n_pages ? -2 : pg;
-      };
-      auto keys = [&](int pg) { return heads + (long long)pg * p.a.b.hkv * 2 * rec; };
-      const int off = tok & (page - 1);
-      const int turn = NG == 4 ? ((off >> 1) & 1) * 2 : 0;  // 16-byte pieces of a value's row change places
-      uint4 kw[kWords], vw[kWords], kp, vp, kp2, vp2;
-      auto load_pairs = [&](int pg, uint4& a, uint4& b) {
-        a = b = make_uint4(0, 0, 0, 0);
-        if (pg < 0) return;
-        const uint8_t* src = keys(pg) + page * (D / 2) + off * (D / 8);
-        if constexpr (NG == 4) {
-          a = *reinterpret_cast<const uint4*>(src);
-          b = *reinterpret_cast<const uint4*>(src + rec);
-        } else {
-          const uint2 a2 = *reinterpret_cast<const uint2*>(src), b2 = *reinterpret_cast<const uint2*>(src + rec);
-          a = make_uint4(a2.x, a2.y, 0, 0);
-          b = make_uint4(b2.x, b2.y, 0, 0);
-        }
-      };
-      auto load_keys = [&](int pg) {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-          kw[i] = pg < 0 ? make_uint4(0, 0, 0, 0)
-                         : reinterpret_cast<const uint4*>(keys(pg) + off * (D / 2))[i];
-      };
-      auto load_values = [&](int pg) {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-          vw[i] = pg < 0 ? make_uint4(0, 0, 0, 0)
-                         : reinterpret_cast<const uint4*>(keys(pg) + rec + off * (D / 2))[i ^ turn];
-      };
-      int pg = look(begin), pg2 = look(begin + 1);
-      load_pairs(pg, kp, vp);
-      load_keys(pg);
-      load_values(pg);
+      const int begin = w.begin(), end = w.end();
       uint32_t ve = 47;  // the values' exponent so far (as bf16 holds it; at least 2^-80)
       if (tok < 4) nan_pos[(item & 3) * 4 + tok] = INT_MAX;
       for (int j = begin; j < end; ++j, ++n) {
-        const int pg3 = look(j + 2);
-        load_pairs(pg2, kp2, vp2);
+        const int vh = kh + 1 == kHalves ? 0 : kh + 1, vph = kh + 1 == kHalves ? kph ^ 1 : kph;
+        if (ok) ok = wait(&c_full[kh], kph);
+        if (ok) ok = wait(&c_full[vh], vph);
+        const unsigned char* kc = ring + kh * C::kHalfBytes;
+        const unsigned char* vc = ring + vh * C::kHalfBytes;
+        // the page's number: -1 behind the last token, -2 where it is not in the cache
+        const int pg = ok ? s_pages[kh * 8 + (tok >> page_log)] : -1;
+        uint4 kp = make_uint4(0, 0, 0, 0), vp = kp;
+        if (pg >= 0 && j * 128 + tok < w.limit()) {
+          const unsigned char* a = kc + page * (D / 2) + off * (D / 8);
+          const unsigned char* b = vc + page * (D / 2) + off * (D / 8);
+          if constexpr (NG == 4) {
+            kp = *reinterpret_cast<const uint4*>(a);
+            vp = *reinterpret_cast<const uint4*>(b);
+          } else {
+            const uint2 a2 = *reinterpret_cast<const uint2*>(a), b2 = *reinterpret_cast<const uint2*>(b);
+            kp.x = a2.x, kp.y = a2.y, vp.x = b2.x, vp.y = b2.y;
+          }
+        }
         // ---- the tile's exponents: of the largest scale or low of its keys, of its values
         uint32_t ka = 0, va = 0;
         const uint32_t pk[4] = {kp.x, kp.y, kp.z, kp.w}, pv[4] = {vp.x, vp.y, vp.z, vp.w};
@@ -481,16 +473,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           }
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {  // d = 128: piece q, words g; d = 64: two pieces of two
-            const uint32_t wd[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+            const int x = (i + first) & (kWords - 1);
+            const uint4 u = reinterpret_cast<const uint4*>(kc + off * (D / 2))[x];
+            const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(dst + chunk_at(tok, i * 4 + k)) =
+              *reinterpret_cast<uint4*>(dst + chunk_at(tok, x * 4 + k)) =
                   unpack8(wd[k], se[k % NG], so[k % NG], lo[k % NG]);
           }
+          mbar_arrive(&c_free[kh]);
           fence_proxy_async_smem();
           mbar_arrive(&k_full[n & 1]);
         }
-        load_keys(pg2);
         // ---- V(n), once PV(n - 2) has: with S(n - 1) in the same item, or the item's last PV
         if (ok && n >= 2) {
           const int it = ended[n & 1];
@@ -521,24 +515,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           }
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
-            const uint32_t wd[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
+            const int x = (i + first) & (kWords - 1);
+            const uint4 u = reinterpret_cast<const uint4*>(vc + off * (D / 2))[x ^ turn];
+            const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(dst + chunk_at(tok, i * 4 + k)) =
+              *reinterpret_cast<uint4*>(dst + chunk_at(tok, x * 4 + k)) =
                   unpack8(wd[k], se[k % (NG / 2)], so[k % (NG / 2)], lo[k % (NG / 2)]);
           }
+          mbar_arrive(&c_free[vh]);
           fence_proxy_async_smem();
           mbar_arrive(&v_full[n & 1]);
         }
-        load_values(pg2);
         ended[n & 1] = j == end - 1 ? item + 1 : 0;
-        kp = kp2;
-        vp = vp2;
-        pg = pg2;
-        pg2 = pg3;
+        kh = vh + 1 == kHalves ? 0 : vh + 1;
+        kph = vh + 1 == kHalves ? vph ^ 1 : vph;
       }
     }
-
     if (!ok && lane == 0 && !*abort_flag) fail();
   } else {
     regs_lower<kRegsIssue>();
@@ -605,6 +598,54 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       umma_commit(drain);
       volatile int never = 0;
       mbar_wait_bounded(drain, 0, &never, kTimeoutNs);
+    }
+    if (warp == 13) {
+      // ================================================================ copies
+      const int page = p.a.b.page, rec = kv4_rec_bytes(page, D), pages = 128 / page;
+      int c = 0;  // halves so far
+      bool ok = true;
+      for (; w.more() && ok; w.next(p)) {
+        const int begin = w.begin(), end = w.end(), limit = w.limit();
+        const int32_t* table = p.a.b.table + (long long)w.b * p.a.b.max_pages;
+        const uint8_t* heads = p.a.cache + (long long)w.head * 2 * rec;
+        // 32 pages looked up at a time, one a lane
+        auto look = [&](int first) {
+          const long long pos = (long long)(first + lane) * page;
+          if (pos >= limit) return -1;
+          const int pg = table[pos / page];
+          return pg < 0 || pg >= p.a.b.n_pages ? -2 : pg;
+        };
+        int chunk = begin * pages, pg = look(chunk);
+        for (int j = begin; ok && j < end; ++j) {
+          if (j * pages - chunk + pages > 32) {
+            chunk = j * pages;
+            pg = look(chunk);
+          }
+          const int x = lane - (j * pages - chunk);  // this lane's page within the tile
+          const bool in = x >= 0 && x < pages, on = in && pg >= 0;
+          const int bytes = rec * __popc(__ballot_sync(0xFFFFFFFFu, on));
+          for (int side = 0; side < 2; ++side, ++c) {
+            const int st = c % kHalves;
+            bool good = true;
+            if (lane == 0 && c >= kHalves) good = wait(&c_free[st], (c / kHalves - 1) & 1);
+            ok = __shfl_sync(0xFFFFFFFFu, good, 0);
+            if (!ok) break;
+            if (in) s_pages[st * 8 + x] = pg;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&c_full[st], bytes);
+            __syncwarp();
+            if (on)
+              bulk_load(smem + C::kOffRing + st * C::kHalfBytes + x * rec,
+                        heads + (long long)pg * p.a.b.hkv * 2 * rec + side * rec, rec, &c_full[st]);
+          }
+        }
+      }
+      if (!ok && lane == 0) {
+        if (!*abort_flag) fail();
+        volatile int never = 0;  // copies still on their way into shared memory
+        for (int i = max(0, c - kHalves); i < c; ++i)
+          mbar_wait_bounded(&c_full[i % kHalves], (i / kHalves) & 1, &never, kTimeoutNs);
+      }
     }
     __syncwarp();
   }
