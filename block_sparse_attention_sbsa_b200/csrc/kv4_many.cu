@@ -68,8 +68,9 @@ struct MC {
   static constexpr int kOffPages = kOffMax + 64;             // int[kHalves][8]: the pages' numbers
   static constexpr int kOffScan = kOffPages + kHalves * 32;
   static constexpr int kOffBar = kOffScan + kScanBytes<kThreads>;
-  // q_full[2] k_full[2] v_full[2] s_bar[2][2] o_bar[2][2] p_full[2] drain c_full[3] c_free[3]
-  static constexpr int kBars = 2 + 2 + 2 + 4 + 4 + 2 + 1 + 2 * kHalves;
+  // q_full[2] k_full[2] v_full[2] s_bar[2][2] o_bar[2][2] p_full[2] p_half[2] drain c_full[3]
+  // c_free[3]
+  static constexpr int kBars = 2 + 2 + 2 + 4 + 4 + 2 + 2 + 1 + 2 * kHalves;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static constexpr uint32_t kDescS = make_idesc(0, 128, 128, false, false);
@@ -81,7 +82,7 @@ struct MC {
 
 // What the softmax has to know of a tile of tokens.
 struct Info {
-  float k_exp;       // logits are S' * 2^k_exp * the row's factor
+  float k_unit;      // logits are S' * k_unit (a power of two) * the row's factor
   int v_exp;         // O's unit after this tile: 2^v_exp
   uint32_t on[4];    // tokens whose page is in the cache
   int pad[2];
@@ -103,6 +104,26 @@ __device__ __forceinline__ uint4 unpack8(uint32_t x, __half2 se, __half2 so, __h
   return r;
 }
 
+// Pairs of fp32 values in one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Offset of chunk c (8 elements) of row `row` in a tile of 128 rows.
 __device__ __forceinline__ int chunk_at(int row, int c) {
   return (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
@@ -121,8 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
   uint64_t* s_bar = bar + 6;       // [tile * 2 + (token tile & 1)]: S(j) and PV(j - 1) done
   uint64_t* o_bar = bar + 10;      // [tile * 2 + (item & 1)]: the item's last PV done
   uint64_t* p_full = bar + 14;     // [tile]
-  uint64_t* drain = bar + 16;
-  uint64_t* c_full = bar + 17;     // [half tile % kHalves]
+  uint64_t* p_half = bar + 16;     // [tile]: the weights of the first 64 tokens
+  uint64_t* drain = bar + 18;
+  uint64_t* c_full = bar + 19;     // [half tile % kHalves]
   uint64_t* c_free = c_full + kHalves;
   int* s_pages = reinterpret_cast<int*>(smem + C::kOffPages);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -138,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       mbar_init(&k_full[i], 128);
       mbar_init(&v_full[i], 128);
       mbar_init(&p_full[i], 128);
+      mbar_init(&p_half[i], 128);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_bar[i], 1);
@@ -257,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         const Info& in = info[n & 3];
-        const float c = f * exp2f(in.k_exp);
+        const float c = f * in.k_unit;
         const int ve = in.v_exp;
         float s[128];
 #pragma unroll
@@ -305,21 +328,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
             tmem_st16(o_col + k, o);
           }
         }
-        float sum[2] = {0.f, 0.f};
+        // (two at a time: packed fp32 operations halve what is issued for all but the exponentials)
+        const uint64_t c2 = pack2(c, c), m2 = pack2(-m, -m);
+        uint64_t sum = pack2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t pk[16];
 #pragma unroll
           for (int y = 0; y < 32; y += 2) {
-            const float p0 = ex2_approx(fmaf(s[k * 32 + y], c, -m));
-            const float p1 = ex2_approx(fmaf(s[k * 32 + y + 1], c, -m));
-            sum[0] += p0;
-            sum[1] += p1;
+            float p0, p1;
+            unpack2(fma2(pack2(s[k * 32 + y], s[k * 32 + y + 1]), c2, m2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum = add2(sum, pack2(p0, p1));
             pk[y >> 1] = h2(__floats2half2_rn(p0, p1));
           }
           tmem_st16u(s_col + k * 16, pk);
+          if (k == 1) {  // PV of the first 64 tokens may begin
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_half[x]);
+          }
         }
-        l += sum[0] + sum[1];
+        float sum0, sum1;
+        unpack2(sum, sum0, sum1);
+        l += sum0 + sum1;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[x]);
@@ -390,8 +423,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     constexpr int kWords = D / 32;  // 16-byte pieces of a row of levels
     const int off = tok & (page - 1);
     const int turn = NG == 4 ? ((off >> 1) & 1) * 2 : 0;  // pieces of a value's row change places
-    // with 4 pieces, neighbouring pairs of tokens begin at different ones: no bank is met twice
-    const int first = NG == 4 ? (tok >> 1) & 3 : 0;
+    // With 4 pieces neighbouring pairs of tokens begin at different ones, so that no bank is met
+    // twice.  Piece `piece[i]`'s words are chunks 4 piece to 4 piece + 3 of the token's row, at
+    // at[i] + word[k] (chunk_at).
+    int piece[kWords], at[kWords], word[4];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      piece[i] = NG == 4 ? (i + (tok >> 1)) & 3 : i;
+      at[i] = (piece[i] >> 1) * (128 * 128) + ((((piece[i] & 1) << 2) ^ (tok & 4)) << 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) word[k] = tok * 128 + ((k ^ (tok & 3)) << 4);
     const unsigned char* ring = smem + C::kOffRing + (tok >> page_log) * rec;
     int n = 0, item = 0;
     int ended[2] = {0, 0};  // by buffer: 1 + the item that ended with its last token tile, else 0
@@ -455,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         if (ok) {
           Info& in = info[n & 3];
           if (tok == 0) {
-            in.k_exp = (float)kn;
+            in.k_unit = exp2f((float)kn);
             in.v_exp = vn;
           }
           if (lane == 0) in.on[warp - 8] = on;
@@ -473,12 +515,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           }
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {  // d = 128: piece q, words g; d = 64: two pieces of two
-            const int x = (i + first) & (kWords - 1);
-            const uint4 u = reinterpret_cast<const uint4*>(kc + off * (D / 2))[x];
+            const uint4 u = reinterpret_cast<const uint4*>(kc + off * (D / 2))[piece[i]];
             const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(dst + chunk_at(tok, x * 4 + k)) =
+              *reinterpret_cast<uint4*>(dst + at[i] + word[k]) =
                   unpack8(wd[k], se[k % NG], so[k % NG], lo[k % NG]);
           }
           mbar_arrive(&c_free[kh]);
@@ -515,12 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           }
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
-            const int x = (i + first) & (kWords - 1);
-            const uint4 u = reinterpret_cast<const uint4*>(vc + off * (D / 2))[x ^ turn];
+            const uint4 u = reinterpret_cast<const uint4*>(vc + off * (D / 2))[piece[i] ^ turn];
             const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(dst + chunk_at(tok, x * 4 + k)) =
+              *reinterpret_cast<uint4*>(dst + at[i] + word[k]) =
                   unpack8(wd[k], se[k % (NG / 2)], so[k % (NG / 2)], lo[k % (NG / 2)]);
           }
           mbar_arrive(&c_free[vh]);
@@ -540,7 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       const uint64_t q0 = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024);
       const uint64_t k0 = smem_desc(smem_u32(smem + C::kOffK), 16, 1024);
       const uint64_t v0 = smem_desc(smem_u32(smem + C::kOffV), 128 * 128, 1024);
-      int n = 0, item = 0, pc[2] = {0, 0}, qc[2] = {0, 0};
+      int n = 0, item = 0;
+      int pc[2] = {0, 0}, hc[2] = {0, 0}, qc[2] = {0, 0};  // phases of p_full, p_half, q_full
       bool ok = true;
       // S of query tile x and token tile t
       auto issue_s = [&](int x, int t) {
@@ -552,10 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           umma_f16_ss(tmem + x * 128, a + at, b + at, C::kDescS, k > 0 ? 1u : 0u);
         }
       };
-      auto issue_pv = [&](int x, int t, bool first) {
+      // O += P V, the first or the second 64 tokens
+      auto issue_pv = [&](int x, int t, bool first, int half) {
         const uint64_t b = v0 + (uint64_t)((t & 1) * (C::kTileBytes >> 4));
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = half * 4; k < half * 4 + 4; ++k)
           umma_f16_ts(tmem + C::kTmO + x * D, tmem + x * 128 + k * 8, b + (uint64_t)(k * 128), C::kDescO,
                       k > 0 || !first ? 1u : 0u);
       };
@@ -566,14 +608,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           // for each query tile: PV(j - 1), then S(j); token tile j is number n
           for (int x = 0; ok && x < 2; ++x) {
             if (j > begin) {
-              ok = wait(&p_full[x], pc[x] & 1);
+              if (x == 0) ok = wait(&v_full[(n - 1) & 1], ((n - 1) >> 1) & 1);
+              if (ok && x < tiles) {
+                ok = wait(&p_half[x], hc[x] & 1);
+                ++hc[x];
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(x, n - 1, j - 1 == begin, 0);
+              }
+              if (ok) ok = wait(&p_full[x], pc[x] & 1);
               ++pc[x];
-              if (ok && x == 0) ok = wait(&v_full[(n - 1) & 1], ((n - 1) >> 1) & 1);
               if (!ok) break;
             }
             if (x < tiles) {
               tc_fence_after();
-              if (j > begin) issue_pv(x, n - 1, j - 1 == begin);
+              if (j > begin) issue_pv(x, n - 1, j - 1 == begin, 1);
               if (j < end) {
                 if (j == begin) {
                   ok = wait(&q_full[x], qc[x] & 1);

@@ -20,6 +20,13 @@ namespace {
 constexpr int kSplitUnit = 128;
 constexpr int kMaxCtas = 160;
 
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+
 struct Part {  // the item whose first part a CTA holds, and its number of parts (0: none)
   int parts, seq, head, tile;
 };
@@ -265,43 +272,53 @@ struct SplitWalk : Items<ROWS> {
 };
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the next
-// ones; a CTA takes every gridDim.y-th row, a thread one place of the slots' rows (channel
-// `place` itself, or as kPermuted says, see kv4_many.cu).
+// ones.  A thread takes 4 places of a slot's row: channels, or what channels kPermuted says
+// (see kv4_many.cu).
+constexpr int kJoinThreads = 256;
+
 template <int D, int ROWS, int SLOT_ROWS, bool kPermuted, typename T>
-__global__ void __launch_bounds__(D) kv4_join_kernel(const __grid_constant__ SplitParams p) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_constant__ SplitParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Part part = p.parts[blockIdx.x];
   if (part.parts < 2) return;
+  const int x = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int c = x % (D / 4) * 4, row = x / (D / 4);
+  if (row >= ROWS) return;
   const Seq s = seq_of(p, part.seq);
-  const int c = threadIdx.x;
-  int channel = c;
-  if (kPermuted)
-    channel = D == 128 ? 32 * (2 * ((c >> 3) & 1) + (c & 1)) + 4 * (c >> 4) + ((c & 7) >> 1)
-                       : 32 * (c & 1) + 4 * (c >> 3) + ((c & 7) >> 1);
+  long long t;
+  int h, i;
+  if (!row_of(p, s, part.head, (long long)part.tile * ROWS + row, &t, &h, &i)) return;
   auto slot = [&](int k) {
     return p.slots + (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) *
                          slot_floats(SLOT_ROWS, D);
   };
-  for (int row = blockIdx.y; row < ROWS; row += gridDim.y) {
-    long long t;
-    int h, i;
-    if (!row_of(p, s, part.head, (long long)part.tile * ROWS + row, &t, &h, &i)) return;
-    float top = -FLT_MAX;
-    for (int k = 0; k < part.parts; ++k) top = fmaxf(top, slot(k)[SLOT_ROWS * D + row]);
-    float acc = 0.f, sum = 0.f;
+  float top = -FLT_MAX;
 #pragma unroll 4
-    for (int k = 0; k < part.parts; ++k) {
-      const float* x = slot(k);
-      const float fac = exp2f(x[SLOT_ROWS * D + row] - top);
-      sum = fmaf(fac, x[SLOT_ROWS * (D + 1) + row], sum);
-      acc = fmaf(fac, x[row * D + c], acc);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    T* dst = static_cast<T*>(p.a.o) + t * p.a.o_token + h * p.a.o_head + channel;
-    if constexpr (sizeof(T) == 4)
-      *dst = acc * inv;
-    else
-      *dst = __float2bfloat16(acc * inv);
+  for (int k = 0; k < part.parts; ++k) top = fmaxf(top, slot(k)[SLOT_ROWS * D + row]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < part.parts; ++k) {
+    const float* y = slot(k);
+    const float4 v = *reinterpret_cast<const float4*>(y + row * D + c);
+    const float fac = exp2f(y[SLOT_ROWS * D + row] - top);
+    sum = fmaf(fac, y[SLOT_ROWS * (D + 1) + row], sum);
+    acc.x = fmaf(fac, v.x, acc.x);
+    acc.y = fmaf(fac, v.y, acc.y);
+    acc.z = fmaf(fac, v.z, acc.z);
+    acc.w = fmaf(fac, v.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  T* dst = static_cast<T*>(p.a.o) + t * p.a.o_token + h * p.a.o_head;
+  if constexpr (kPermuted) {
+    // places c to c + 3: channels u and u + 1 of two neighbouring groups
+    const int u = D == 128 ? 64 * ((c >> 3) & 1) + 4 * (c >> 4) + ((c & 7) >> 1)
+                           : 4 * (c >> 3) + ((c & 7) >> 1);
+    *reinterpret_cast<__nv_bfloat162*>(dst + u) = __floats2bfloat162_rn(acc.x, acc.z);
+    *reinterpret_cast<__nv_bfloat162*>(dst + u + 32) = __floats2bfloat162_rn(acc.y, acc.w);
+  } else {
+    store4(dst + c, acc);
   }
 }
 
@@ -313,8 +330,8 @@ int launch_join(const SplitParams& p, int grid, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, ROWS < 16 ? ROWS : 16);
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = dim3(grid, (ROWS * (D / 4) + kJoinThreads - 1) / kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
