@@ -76,7 +76,7 @@ Kv4Batch batch(const sbsa_kv4_params* p, const int32_t* table, const int32_t* le
 // 16, but spends less on what it reads.
 bool many_rows(const sbsa_kv4_params* p) {
   return p->dtype == SBSA_BF16 && !p->list_heads &&
-         (long long)p->max_new * (p->n_q_heads / p->n_kv_heads) > 32;
+         (long long)p->max_new * (p->n_q_heads / p->n_kv_heads) > 48;
 }
 
 int cuda_code(cudaError_t e) { return e == cudaSuccess ? SBSA_OK : SBSA_ERR_CUDA; }
