@@ -46,7 +46,7 @@ namespace {
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kUnit = kSplitUnit;  // tokens of a stage
 // What an item costs a CTA besides its units (rows, joining, output), in units.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = 6;
 // Weights are 2^(S - M), M = (reference of the logits) + (reference of the
 // values' exponents) - kHead; each reference moves only when it is outgrown by more
 // than kLazy, so the fp16 weights times a scale stay below 2^(kHead + 2 kLazy + 1) = 2^15.

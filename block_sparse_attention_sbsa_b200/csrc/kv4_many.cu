@@ -44,7 +44,7 @@ namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kRows = 256;  // of an item: two tiles of 128
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 5;
 constexpr int kThreads = 512;
 // 256 * 184 + 128 * 80 + 128 * 64 = 512 * 128, what the block is launched with
 constexpr int kRegsSoftmax = 184, kRegsUnpack = 80, kRegsIssue = 64;
