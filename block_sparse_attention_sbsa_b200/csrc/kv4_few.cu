@@ -4,11 +4,11 @@
 // Mathematics.  With a key's group g of 32 channels as low + scale * n, a
 // row's logit is  sum_g scale[t, g] (q_g . n[t, g]) + low[t, g] sum(q_g),  and
 // its output  sum_t P[t] scale[t, g] n[t, c] + sum_t P[t] low[t, g]  over
-// sum_t P[t]: the products take the levels n as they lie in memory, and scales
-// and lows enter per (row, token, group) in fp32.  A 4-bit level in the low
-// bits of a 16-bit word is the fp16 denormal n 2^-24, exactly; at bit 4 it is
-// 16 n 2^-24.  So a fragment register of two levels costs one AND (and half a
-// shift), no conversion: the powers of two are folded into q and the output.
+// sum_t P[t]: the products take the levels n, and scales and lows enter per (row,
+// token, group) in fp32.  A 4-bit level in the low bits of a 16-bit word is the
+// fp16 denormal n 2^-24, exactly; at bit 4 it is 16 n 2^-24.  So a fragment
+// register of two levels costs one AND (and half a shift), no conversion: the powers
+// of two are folded into q and the output.  (The values' levels are taken less 8.)
 //
 // Bound: HBM, 5/4 d bytes a token and kv head.  At 6.5 TB/s an SM has about
 // 110 cycles for 16 tokens (d = 128, 2560 bytes), and the work on them is
@@ -129,6 +129,21 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two levels (the bits in MASK, times 16 in the upper one) less N.  As fp16 denormals, in units
+// of 2^-24, they cost an AND and an exact subtraction; but the tensor cores align products by
+// the operands' exponents, and a denormal's leading zeros are then missing at the other end:
+// 18 bits are left of a sum.  That is enough for bf16 rows.  For fp32 rows (kExact) they are made
+// normal numbers: OR into the mantissa of 1024 before the subtraction.
+template <bool kExact, uint32_t MASK, int N>
+__device__ __forceinline__ uint32_t less(uint32_t x) {
+  uint32_t y = x & MASK;
+  if (!kExact && N == 0) return y;
+  if (kExact) y |= 0x64006400u;
+  const __half n = __ushort_as_half((unsigned short)((kExact ? 0x6400 : 0) + N));
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&y), __half2half2(n));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ float scale_of(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float low_of(uint32_t pair) {
   return __uint_as_float(pair & 0xFFFF0000u);
@@ -190,6 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   constexpr int ROWS = C::kRows;
   constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
   constexpr int TT = C::kSub;
+  constexpr bool kExact = PARTS == 2;
+  constexpr int kUnitLog2 = kExact ? 0 : 24;  // levels enter the products in units of 2^-kUnitLog2
   extern __shared__ __align__(128) unsigned char smem[];
   float* s_out = reinterpret_cast<float*>(smem + C::kOffOut);
   float* s_stat = reinterpret_cast<float*>(smem + C::kOffStat);
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     // ---- the query rows as fragments: elements (0, 4), (1, 5)/16, (2, 6), (3, 7)/16 of each 8
     // channels, as the levels come out of a word
     uint32_t bq[NT][PARTS][NG][2][2];
-    // sum(q_g) 2^-24 in three bf16 parts, against the lows of two groups a lane: with 4 groups
+    // sum(q_g) (in the products' unit) in three bf16 parts, against the lows of two groups a lane: with 4 groups
     // k-pairs q = 0, 1 hold the first part of groups (0, 1) and (2, 3), 2 and 3 the second, 8 behind
     // them the third; with 2 groups q = 0, 1, 2 hold the three parts
     uint32_t bl[NT][2];
@@ -349,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
       const int e = clamp_int(137 - (int)(__float_as_uint(mx) >> 23), -90, 100);
       const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-      const float fr = p.scale_log2 * __uint_as_float((uint32_t)(24 - e + 127) << 23);
+      const float fr = p.scale_log2 * __uint_as_float((uint32_t)(kUnitLog2 - e + 127) << 23);
       // rows that see nothing (before the sequence, beyond max_new) mask all; rows past the
       // tile's last mask nothing, so that they never send the warp to the masked path
       int lr = INT_MAX;
@@ -375,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
         }
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        qs[g] = sum * 0x1p-24f;
+        qs[g] = sum * (kUnitLog2 ? 0x1p-24f : 1.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float sc = (j & 1) ? 0.0625f : 1.f;
@@ -411,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
 
     // rows' references: ms for the logits, me (an exponent as bf16 holds it) for the magnitude of the
     // values, common to all rows; weights are 2^(logit - m), m = ms + (me - 127) - kHead.
-    // o: outputs; ol: the lows' sums of this lane's tokens, l: their weights' sums
+    // o: outputs; ol: the sums of this lane's tokens' low + 8 scale, l: of their weights
     float o[NT][NG][2][4], ol[NT][NG][2], l[NT][2], m[NT][2], ms[NT][2];
     uint32_t me = 0, big = 0;
 #pragma unroll
@@ -470,8 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const uint32_t x0 = w0.w[g], x1 = w1.w[g], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t f0[4] = {x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u};
-          const uint32_t f1[4] = {y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u};
+          const uint32_t f0[4] = {less<kExact, 0x000F000Fu, 0>(x0), less<kExact, 0x000F000Fu, 0>(x1),
+                                  less<kExact, 0x00F000F0u, 0>(x0), less<kExact, 0x00F000F0u, 0>(x1)};
+          const uint32_t f1[4] = {less<kExact, 0x000F000Fu, 0>(y0), less<kExact, 0x000F000Fu, 0>(y1),
+                                  less<kExact, 0x00F000F0u, 0>(y0), less<kExact, 0x00F000F0u, 0>(y1)};
           const float s0 = scale_of(p0.w[g]), s1 = scale_of(p1.w[g]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -575,10 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
           const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
           const uint32_t x0 = __byte_perm(va0.w[g >> 1], vb0.w[g >> 1], sel), y0 = x0 >> 8;
           const uint32_t x1 = __byte_perm(va1.w[g >> 1], vb1.w[g >> 1], sel), y1 = x1 >> 8;
-          const uint32_t f0[4] = {x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u};
-          const uint32_t f1[4] = {y0 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x000F000Fu, y1 & 0x00F000F0u};
+          // level - 8, and the lows' sums below take low + 8 scale: the levels alone would make
+          // sums that only grow, which the tensor cores cut off at every step and the lows then
+          // cancel (over 500,000 tokens 5e-6 of the values, three times the output's rounding)
+          const uint32_t f0[4] = {less<kExact, 0x000F000Fu, 8>(x0), less<kExact, 0x00F000F0u, 128>(x0),
+                                  less<kExact, 0x000F000Fu, 8>(x1), less<kExact, 0x00F000F0u, 128>(x1)};
+          const uint32_t f1[4] = {less<kExact, 0x000F000Fu, 8>(y0), less<kExact, 0x00F000F0u, 128>(y0),
+                                  less<kExact, 0x000F000Fu, 8>(y1), less<kExact, 0x00F000F0u, 128>(y1)};
           const float sc[2] = {scale_of(pv[tt][0].w[g]), scale_of(pv[tt][1].w[g])};
-          const float lw[2] = {low_of(pv[tt][0].w[g]), low_of(pv[tt][1].w[g])};
+          const float lw[2] = {fmaf(8.f, sc[0], low_of(pv[tt][0].w[g])),
+                               fmaf(8.f, sc[1], low_of(pv[tt][1].w[g]))};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float x[4];
@@ -642,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     base_n += end - begin;
     if (!ok && lane == 0 && !*abort_flag) fail();
 
+    constexpr float kUnit = kExact ? 1.f : 0x1p24f;
     // ---- join the 8 warps: each leaves its rows' outputs and sums in shared memory
     consumers_sync<kWarps * 32>();  // the previous item's have been read
 #pragma unroll
@@ -652,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
         for (int c = 0; c < 2; ++c) {
           float* dst = s_out + (warp * ROWS + nt * 8 + 2 * q + c) * C::kOutStride + g * 32 + r * 4;
           *reinterpret_cast<float4*>(dst) =
-              make_float4(o[nt][g][0][c] * 0x1p24f, o[nt][g][0][2 + c] * 0x1p20f,
-                          o[nt][g][1][c] * 0x1p24f, o[nt][g][1][2 + c] * 0x1p20f);
+              make_float4(o[nt][g][0][c] * kUnit, o[nt][g][0][2 + c] * (kUnit / 16),
+                          o[nt][g][1][c] * kUnit, o[nt][g][1][2 + c] * (kUnit / 16));
         }
       }
       // the sums over the lanes' tokens
