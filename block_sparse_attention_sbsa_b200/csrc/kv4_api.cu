@@ -35,6 +35,10 @@ int validate_attend(const sbsa_kv4_params* p) {
   if (p->max_new < 1) return SBSA_ERR_INVALID_ARG;
   if (!(p->sm_scale >= 0.f) || !std::isfinite(p->sm_scale)) return SBSA_ERR_INVALID_ARG;
   if (p->n_q_heads > 65535) return SBSA_ERR_UNSUPPORTED;
+  // rows and (sequence, head) pairs are numbered in 32 bits
+  if ((long long)p->n_tokens * p->n_q_heads > 0x7FFF0000LL ||
+      (long long)p->n_seqs * p->n_q_heads > 0x7FFF0000LL)
+    return SBSA_ERR_UNSUPPORTED;
   if (p->list_heads) {
     if (p->list_heads != p->n_kv_heads && p->list_heads != p->n_q_heads)
       return SBSA_ERR_INVALID_ARG;

@@ -315,7 +315,7 @@ using namespace sbsa;
 
 extern "C" {
 
-int sbsa_version(void) { return 104; }
+int sbsa_version(void) { return 105; }
 
 const char* sbsa_status_string(int code) {
   switch (code) {

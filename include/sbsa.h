@@ -518,7 +518,9 @@ int sbsa_kv4_read(const sbsa_kv4_params* p, const void* cache, const int32_t* pa
                   void* stream);
 
 /* Device workspace of sbsa_kv4_attend: partial results of the rows whose
- * tokens are shared out over several CTAs.  0 when p is invalid. */
+ * tokens are shared out over several CTAs.  It depends on head_dim and on whether
+ * a kv head has more than 48 rows (max_new * Hq / Hkv; bf16, without lists): 1.4 or 22 MB
+ * at d = 64, 2.7 or 43 MB at d = 128, and not on the batch.  0 when p is invalid. */
 size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
 
 /*
@@ -538,8 +540,13 @@ size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
  * 0.  Listed blocks outside the sequence, pages outside the cache, and rows out
  * of range are skipped (o is 0 there) and reported as SBSA_ERR_DEVICE; a
  * repeated block is attended twice.
- * Errors as sbsa_kv4_append, and SBSA_ERR_WORKSPACE for a missing, misaligned
- * or short workspace.
+ * Precision: products in fp16 with fp32 accumulation, exact up to the rounding of the
+ * weights (2^-11 of each; fp32 rows take both operands in two parts, 2^-22) and, for
+ * more than 48 rows of a kv head, of the dequantised keys and values (2^-11).  Results
+ * do not change between runs.
+ * Errors as sbsa_kv4_append, SBSA_ERR_UNSUPPORTED also for n_tokens * Hq or n_seqs * Hq
+ * above 2^31 - 2^16, and SBSA_ERR_WORKSPACE for a missing, misaligned or short
+ * workspace.
  */
 int sbsa_kv4_attend(const sbsa_kv4_params* p, const void* cache, const int32_t* page_table,
                     const int32_t* seq_lens, const int32_t* cu_new, const void* q,

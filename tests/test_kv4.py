@@ -84,6 +84,7 @@ def test_every_operator_refuses(kv4, change, code):
     (dict(list_heads=2, block_size=32, max_blocks=1), 2),
     (dict(list_heads=2, block_size=64, max_blocks=1, page_size=128), 1),   # half a page
     (dict(list_heads=2, block_size=128, max_blocks=1 << 24), 2),
+    (dict(n_tokens=1 << 29), 2), (dict(n_seqs=1 << 29), 2),
 ])
 def test_attend_refuses(kv4, change, code):
     p = _params(kv4, **change)
@@ -432,6 +433,93 @@ def test_attend_reports_what_is_out_of_range(kv4, cuda):
     out.fill_(5.0)
     kv4.attend(b.g_cache, q, *b.g, 4, out=out)
     assert _status(kv4) == 6 and (out[:, 2:4] == 0).all() and torch.isfinite(out).all()
+
+
+@pytest.mark.gpu
+def test_attend_many_rows_reports_what_is_out_of_range(kv4, cuda):
+    """The same for a chunk of more rows than the few-row kernel takes: a page outside the cache in the middle
+    of a tile, rows beyond max_new, rows before the sequence's first token, in two query tiles."""
+    rng = np.random.default_rng(6)
+    page, d, hkv, hq, n, new = 16, 64, 1, 4, 300, 60
+    b = _fast_fill(Batch([n, 90], [new, new], page, hkv, d, seed=6), rng).gpu()
+    q = _rows(rng, hq, b.total, d, "bf16", True)
+    out = torch.zeros_like(q)
+    b.g[0][0, 9] = b.pages + 3
+    kv4.attend(b.g_cache, q, *b.g, new, out=out)
+    assert _status(kv4) == 6
+    k, v = (x[:, 0].astype(np.float64) for x in KP.tokens(KP.decode(b.cache), b.table[0], n))
+    for h in range(hq):
+        for t in (0, 31, 59):
+            keep = np.array([u for u in range(n - new + t + 1) if not 144 <= u < 160])
+            s = k[keep] @ q[h, t].double().cpu().numpy() / 8
+            p = np.exp(s - s.max())
+            assert np.abs(out[h, t].double().cpu().numpy() - p @ v[keep] / p.sum()).max() < 0.02
+    b.g[0].copy_(torch.from_numpy(b.table))
+    out.fill_(5.0)
+    kv4.attend(b.g_cache, q, *b.g, 50, out=out)
+    assert _status(kv4) == 6
+    assert (out[:, 50:60] == 0).all() and (out[:, 110:] == 0).all()
+    _check_rows = np.r_[0:50, 60:110]
+    want, size, span = KP.attend(KP.decode(b.cache), q.float().cpu().numpy(), b.table, b.lens, b.cu)
+    err = np.abs(out.float().cpu().numpy() - want)[:, _check_rows]
+    assert (err <= _tolerance(want, size, span, "bf16", n, d)[:, _check_rows]).all()
+    b.g[1][1] = 20
+    out.fill_(5.0)
+    kv4.attend(b.g_cache, q, *b.g, new, out=out)
+    assert _status(kv4) == 6 and (out[:, 60:100] == 0).all() and (out[:, 100:] != 0).any(dim=-1).all()
+    b.g[1].fill_(0)
+    kv4.attend(b.g_cache, q, *b.g, new, out=out)
+    assert _status(kv4) == 6 and (out == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_attend_long_contexts_have_no_drift(kv4, cuda, dtype):
+    """Over many tokens the output is a small mean of large values, so an error that does not average out
+    shows.  Each row's error, over channels, has a 2-norm below: fp32, 2^-22 of the values' (a bit of the
+    weights' two parts) plus 2^-21 of the output's; bf16, its rounding 2^-9 of the output in the mean
+    (uniform up to 2^-8) plus 2^-11 of the values' over the square root of the tokens that count, plus
+    2^-18 of the values' for sums in 18 bits."""
+    d, n, hq = 128, 60000, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v, q = (torch.randn(h, t, d, generator=g, device="cuda").to(DT[dtype]) for h, t in ((1, n), (1, n), (hq, 1)))
+    pages = -(-n // 64)
+    cache = kv4.empty(pages, 1, 64, d)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    lens, cu, one = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n], [0, n], [0, 1]))
+    kv4.append(cache, k, v, table, lens, cu)
+    kr, vr = (torch.empty(1, n, d, device="cuda") for _ in range(2))
+    kv4.read(cache, table, lens, cu, k_out=kr, v_out=vr)
+    o = kv4.attend(cache, q, table, lens, one, 1)[:, 0].double()
+    p = torch.softmax(q[:, 0].double() @ kr[0].double().T / d ** 0.5, -1)
+    want = p @ vr[0].double()
+    err, size = (o - want).norm(dim=-1), vr[0].double().norm(dim=-1).mean()
+    if dtype == "fp32":
+        assert (err <= 2.0 ** -22 * size + 2.0 ** -21 * want.norm(dim=-1)).all(), err / size
+    else:
+        spread = p.square().sum(-1).sqrt()
+        assert (err <= 2.0 ** -9 * want.norm(dim=-1) + (2.0 ** -11 * spread + 2.0 ** -18) * size).all(), err / size
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(kv4, cuda):
+    """Calls that overlap, few and many rows, each with its own workspace."""
+    rng = np.random.default_rng(13)
+    b = _fast_fill(Batch([3000, 500, 1200], [1, 1, 1], 64, 2, 128, seed=13), rng).gpu()
+    c = _fast_fill(Batch([2000, 700], [300, 41], 32, 2, 128, seed=14), rng).gpu()
+    q, r = _rows(rng, 8, 3, 128, "bf16", True), _rows(rng, 8, c.total, 128, "bf16", True)
+    one, two = kv4.attend(b.g_cache, q, *b.g, 1), kv4.attend(c.g_cache, r, *c.g, 300)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got.append(kv4.attend(b.g_cache, q, *b.g, 1, stream=s) if i % 2 else
+                       kv4.attend(c.g_cache, r, *c.g, 300, stream=s))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, one if i % 2 else two)
+    assert _status(kv4) == 0
 
 
 @pytest.mark.gpu
