@@ -715,7 +715,7 @@ int launch(const SplitParams& p, cudaStream_t stream) {
   if (grid <= 0) return SBSA_ERR_CUDA;
   kern<<<grid, kThreads, C::kSmem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SBSA_ERR_CUDA;
-  return launch_join<D, kRows, kRows, true, __nv_bfloat16>(p, grid, stream);
+  return launch_join<D, kRows>(p, grid, stream);
 }
 
 }  // namespace

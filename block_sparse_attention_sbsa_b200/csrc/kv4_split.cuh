@@ -10,6 +10,7 @@
 #pragma once
 #include <atomic>
 #include <cfloat>
+#include <chrono>
 
 #include "kv4.cuh"
 #include "tma_map.h"
@@ -36,7 +37,7 @@ struct Part {  // the item whose first part a CTA holds, and its number of parts
 constexpr size_t slot_floats(int rows, int d) { return (size_t)rows * (d + 2); }
 
 inline size_t split_workspace(int rows, int d) {
-  return kMaxCtas * (2 * slot_floats(rows, d) * sizeof(float) + sizeof(Part));
+  return kMaxCtas * (2 * (slot_floats(rows, d) * sizeof(float) + sizeof(uint64_t)) + sizeof(Part));
 }
 
 struct SplitParams {
@@ -48,7 +49,20 @@ struct SplitParams {
   float* slots;      // two a CTA: of the item that begins before its run, and of the one that
                      // goes on behind it
   Part* parts;       // one a CTA
+  uint64_t* ready;   // one a slot: `call` once the slot holds its part (see kv4_few.cu)
+  uint64_t call;
 };
+
+// A number that no other call has (and that memory which no call has written does not hold by
+// chance).
+inline uint64_t call_number() {
+  static std::atomic<uint64_t> next{
+      (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count()};
+  uint64_t z = (next.fetch_add(1) + 1) * 0x9E3779B97F4A7C15ull;  // splitmix64 (Steele, Lea, Flood)
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return (z ^ (z >> 31)) | 1;
+}
 
 inline SplitParams split_params(const Kv4AttendArgs& a, int slot_rows) {
   SplitParams p{};
@@ -59,6 +73,7 @@ inline SplitParams split_params(const Kv4AttendArgs& a, int slot_rows) {
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   p.slots = static_cast<float*>(a.workspace);
   p.parts = reinterpret_cast<Part*>(p.slots + kMaxCtas * 2 * slot_floats(slot_rows, a.d));
+  p.ready = reinterpret_cast<uint64_t*>(p.parts + kMaxCtas);
   return p;
 }
 
@@ -262,6 +277,11 @@ struct SplitWalk : Items<ROWS> {
     }
     set(p);
   }
+  // The CTA that owns the item's first unit.
+  __device__ int first_cta(const Run& r) const {
+    const long long first = r.end - left + COST;
+    return (int)(((first + 1) * r.ctas + r.total - 1) / r.total) - 1;
+  }
   // The CTA's entry of p.parts for an item that begins here and goes on in the next
   // CTAs, up to the one that owns its last unit.
   __device__ Part part(const Run& r, int cta) const {
@@ -272,11 +292,10 @@ struct SplitWalk : Items<ROWS> {
 };
 
 // Joins the parts of the item that begins in CTA blockIdx.x and goes on in the next
-// ones.  A thread takes 4 places of a slot's row: channels, or what channels kPermuted says
-// (see kv4_many.cu).
+// ones (kv4_many.cu).  A thread takes 4 places of a slot's row.
 constexpr int kJoinThreads = 256;
 
-template <int D, int ROWS, int SLOT_ROWS, bool kPermuted, typename T>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_constant__ SplitParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Part part = p.parts[blockIdx.x];
@@ -290,19 +309,19 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
   if (!row_of(p, s, part.head, (long long)part.tile * ROWS + row, &t, &h, &i)) return;
   auto slot = [&](int k) {
     return p.slots + (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) *
-                         slot_floats(SLOT_ROWS, D);
+                         slot_floats(ROWS, D);
   };
   float top = -FLT_MAX;
 #pragma unroll 4
-  for (int k = 0; k < part.parts; ++k) top = fmaxf(top, slot(k)[SLOT_ROWS * D + row]);
+  for (int k = 0; k < part.parts; ++k) top = fmaxf(top, slot(k)[ROWS * D + row]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
 #pragma unroll 4
   for (int k = 0; k < part.parts; ++k) {
     const float* y = slot(k);
     const float4 v = *reinterpret_cast<const float4*>(y + row * D + c);
-    const float fac = exp2f(y[SLOT_ROWS * D + row] - top);
-    sum = fmaf(fac, y[SLOT_ROWS * (D + 1) + row], sum);
+    const float fac = exp2f(y[ROWS * D + row] - top);
+    sum = fmaf(fac, y[ROWS * (D + 1) + row], sum);
     acc.x = fmaf(fac, v.x, acc.x);
     acc.y = fmaf(fac, v.y, acc.y);
     acc.z = fmaf(fac, v.z, acc.z);
@@ -310,20 +329,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  T* dst = static_cast<T*>(p.a.o) + t * p.a.o_token + h * p.a.o_head;
-  if constexpr (kPermuted) {
-    // places c to c + 3: channels u and u + 1 of two neighbouring groups
-    const int u = D == 128 ? 64 * ((c >> 3) & 1) + 4 * (c >> 4) + ((c & 7) >> 1)
-                           : 4 * (c >> 3) + ((c & 7) >> 1);
-    *reinterpret_cast<__nv_bfloat162*>(dst + u) = __floats2bfloat162_rn(acc.x, acc.z);
-    *reinterpret_cast<__nv_bfloat162*>(dst + u + 32) = __floats2bfloat162_rn(acc.y, acc.w);
-  } else {
-    store4(dst + c, acc);
-  }
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.o) + t * p.a.o_token + h * p.a.o_head;
+  // places c to c + 3: channels u and u + 1 of two neighbouring groups
+  const int u = D == 128 ? 64 * ((c >> 3) & 1) + 4 * (c >> 4) + ((c & 7) >> 1)
+                         : 4 * (c >> 3) + ((c & 7) >> 1);
+  *reinterpret_cast<__nv_bfloat162*>(dst + u) = __floats2bfloat162_rn(acc.x, acc.z);
+  *reinterpret_cast<__nv_bfloat162*>(dst + u + 32) = __floats2bfloat162_rn(acc.y, acc.w);
 }
 
 // Behind the attending kernel, which lets it start up early.
-template <int D, int ROWS, int SLOT_ROWS, bool kPermuted, typename T>
+template <int D, int ROWS>
 int launch_join(const SplitParams& p, int grid, cudaStream_t stream) {
   if (!split_possible(p.a)) return SBSA_OK;
   cudaLaunchAttribute attr;
@@ -335,7 +350,7 @@ int launch_join(const SplitParams& p, int grid, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, ROWS, SLOT_ROWS, kPermuted, T>, p) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, ROWS>, p) == cudaSuccess
              ? SBSA_OK
              : SBSA_ERR_CUDA;
 }
