@@ -55,9 +55,9 @@ struct Kv4AttendArgs {
 // The two kernels of the attention, and the bytes of their partial results: for few
 // rows a sequence (all types, with lists), and for many (bf16, without lists).
 // The launchers return an SBSA_* code.
-size_t kv4_few_workspace(int d);
+size_t kv4_few_workspace(const Kv4AttendArgs& a);
 int launch_kv4_few(const Kv4AttendArgs& a, cudaStream_t stream);
-size_t kv4_many_workspace(int d);
+size_t kv4_many_workspace(const Kv4AttendArgs& a);
 int launch_kv4_many(const Kv4AttendArgs& a, cudaStream_t stream);
 
 }  // namespace sbsa

@@ -83,6 +83,30 @@ bool many_rows(const sbsa_kv4_params* p) {
          (long long)p->max_new * (p->n_q_heads / p->n_kv_heads) > 48;
 }
 
+// The sizes that the launchers go by (no pointers).
+Kv4AttendArgs attend_sizes(const sbsa_kv4_params* p) {
+  Kv4AttendArgs a{};
+  a.b.n_seqs = p->n_seqs;
+  a.b.n_tokens = p->n_tokens;
+  a.b.max_pages = p->max_pages;
+  a.b.n_pages = p->n_pages;
+  a.b.page = p->page_size;
+  a.b.hkv = p->n_kv_heads;
+  a.hq = p->n_q_heads;
+  a.d = p->head_dim;
+  a.dtype = p->dtype;
+  a.max_new = p->max_new;
+  a.list_heads = p->list_heads;
+  a.block = p->block_size;
+  a.max_blocks = p->max_blocks;
+  return a;
+}
+
+size_t attend_workspace(const sbsa_kv4_params* p) {
+  const Kv4AttendArgs a = attend_sizes(p);
+  return many_rows(p) ? kv4_many_workspace(a) : kv4_few_workspace(a);
+}
+
 int cuda_code(cudaError_t e) { return e == cudaSuccess ? SBSA_OK : SBSA_ERR_CUDA; }
 
 }  // namespace
@@ -145,7 +169,7 @@ int sbsa_kv4_read(const sbsa_kv4_params* p, const void* cache, const int32_t* pa
 
 size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p) {
   if (validate_attend(p) != SBSA_OK) return 0;
-  return many_rows(p) ? kv4_many_workspace(p->head_dim) : kv4_few_workspace(p->head_dim);
+  return attend_workspace(p);
 }
 
 int sbsa_kv4_attend(const sbsa_kv4_params* p, const void* cache, const int32_t* page_table,
@@ -163,10 +187,10 @@ int sbsa_kv4_attend(const sbsa_kv4_params* p, const void* cache, const int32_t* 
     return SBSA_ERR_INVALID_ARG;
   if (p->list_heads ? (!idx || !cnt) : (idx || cnt)) return SBSA_ERR_INVALID_ARG;
   if (!aligned16(cache) || !aligned16(q) || !aligned16(o)) return SBSA_ERR_INVALID_ARG;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      ws_bytes < sbsa_kv4_attend_workspace_bytes(p))
+  const size_t need = attend_workspace(p);
+  if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < need))
     return SBSA_ERR_WORKSPACE;
-  Kv4AttendArgs a{};
+  Kv4AttendArgs a = attend_sizes(p);
   a.b = batch(p, page_table, seq_lens, cu_new);
   a.cache = static_cast<const uint8_t*>(cache);
   a.q = Kv4Rows{q, q_token_stride, q_head_stride};
@@ -175,13 +199,6 @@ int sbsa_kv4_attend(const sbsa_kv4_params* p, const void* cache, const int32_t* 
   a.o_head = o_head_stride;
   a.idx = idx;
   a.cnt = cnt;
-  a.hq = p->n_q_heads;
-  a.d = p->head_dim;
-  a.dtype = p->dtype;
-  a.max_new = p->max_new;
-  a.list_heads = p->list_heads;
-  a.block = p->block_size;
-  a.max_blocks = p->max_blocks;
   a.sm_scale = p->sm_scale > 0.f ? p->sm_scale : 1.0f / std::sqrt((float)p->head_dim);
   a.workspace = workspace;
   auto launch = many_rows(p) ? launch_kv4_many : launch_kv4_few;

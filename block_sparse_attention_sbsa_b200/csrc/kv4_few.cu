@@ -848,7 +848,9 @@ int launch(const SplitParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t kv4_few_workspace(int d) { return split_workspace(kSlotRows, d); }
+size_t kv4_few_workspace(const Kv4AttendArgs& a) {
+  return split_possible(a) ? split_workspace(kSlotRows, a.d) : 0;
+}
 
 int launch_kv4_few(const Kv4AttendArgs& a, cudaStream_t stream) {
   SplitParams p = split_params(a, kSlotRows);

@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x == 0) p.parts[blockIdx.x].parts = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may start up
   Run run;
   if (!split_run<kRows, kItemCost, kThreads>(p, reinterpret_cast<long long*>(smem + C::kOffScan), &run))
     return;
@@ -720,7 +722,7 @@ int launch(const SplitParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t kv4_many_workspace(int d) { return split_workspace(kRows, d); }
+size_t kv4_many_workspace(const Kv4AttendArgs& a) { return split_workspace(kRows, a.d); }
 
 int launch_kv4_many(const Kv4AttendArgs& a, cudaStream_t stream) {
   const SplitParams p = split_params(a, kRows);

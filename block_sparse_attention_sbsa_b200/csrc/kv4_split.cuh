@@ -96,7 +96,8 @@ struct SplitGrid {
   }
 };
 
-// Whether an item can have more than one unit, and so more than one CTA.
+// Whether an item can have more than one unit, and so more than one CTA: else there
+// is nothing to join, and no workspace.
 inline bool split_possible(const Kv4AttendArgs& a) {
   if (a.list_heads) return (long long)a.max_blocks * a.block > kSplitUnit;
   return (long long)a.b.max_pages * a.b.page > kSplitUnit;
@@ -175,7 +176,7 @@ constexpr int kScanBytes = (THREADS / 32 + 2) * 8 + 16;
 
 // All threads of the CTA together, with kScanBytes of shared memory; false when
 // the CTA has no run.  Ends with the CTA in step (earlier writes to shared memory are
-// visible).  Also clears the CTA's entry of p.parts, and lets the joining kernel start up.
+// visible).
 template <int ROWS, int COST, int THREADS>
 __device__ __forceinline__ bool split_run(const SplitParams& p, long long* s_scan, Run* run) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -201,8 +202,6 @@ __device__ __forceinline__ bool split_run(const SplitParams& p, long long* s_sca
   }
   const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
   const int cta = blockIdx.x;
-  if (threadIdx.x == 0) p.parts[cta].parts = 0;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (cta >= ctas) return false;
   run->ctas = ctas;
   run->total = total;

@@ -52,6 +52,7 @@ lib.sbsa_kv4_attend.argtypes = [_PP, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _
 lib.sbsa_kv4_attend.restype = ctypes.c_int
 
 _append, _read, _attend = lib.sbsa_kv4_append, lib.sbsa_kv4_read, lib.sbsa_kv4_attend
+_workspace_bytes = lib.sbsa_kv4_attend_workspace_bytes
 
 _DTYPE = {torch.bfloat16: BF16, torch.float32: FP32}
 
@@ -212,25 +213,26 @@ def attend(cache, q, page_table, seq_lens, cu_new, max_new: int, idx=None, cnt=N
             raise ValueError(f"cnt must be contiguous int32 {tuple(idx.shape[:2])} on cuda:{dev}")
         p.list_heads, p.max_blocks, p.block_size = idx.shape[1], idx.shape[2], block_size
         lists = (idx.data_ptr(), cnt.data_ptr())
+    size = 0
     if workspace is None:
-        size = attend_workspace_bytes(p)
-        if stream is None:
-            workspace = torch.empty(size, dtype=_U8, device=cache.device)
-        else:  # with the call's stream current: the memory is not given away before it has run
-            with torch.cuda.stream(stream):
+        size = _workspace_bytes(p)  # 0: none is needed (or the call below refuses p)
+        if size:
+            if stream is None:
                 workspace = torch.empty(size, dtype=_U8, device=cache.device)
+            else:  # with the call's stream current: the memory is not given away before it has run
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(size, dtype=_U8, device=cache.device)
     elif workspace.dtype is not _U8 or not workspace.is_contiguous() \
             or workspace.get_device() != dev:
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
+    else:
+        size = workspace.numel()
     _call(_attend, "sbsa_kv4_attend", dev, stream, p, cache.data_ptr(), page_table.data_ptr(),
           seq_lens.data_ptr(), cu_new.data_ptr(), q.data_ptr(), *qr, out.data_ptr(), *orow, *lists,
-          workspace.data_ptr(), workspace.numel())
+          None if workspace is None else workspace.data_ptr(), size)
     return out
 
 
 def attend_workspace_bytes(p: Params) -> int:
-    """Bytes of the workspace of `attend`."""
-    n = lib.sbsa_kv4_attend_workspace_bytes(p)
-    if n == 0:
-        raise SbsaError(ERR_INVALID_ARG, "sbsa_kv4_attend_workspace_bytes")
-    return n
+    """Bytes of the workspace of `attend`; 0 where it needs none (or refuses p)."""
+    return _workspace_bytes(p)

@@ -520,7 +520,9 @@ int sbsa_kv4_read(const sbsa_kv4_params* p, const void* cache, const int32_t* pa
 /* Device workspace of sbsa_kv4_attend: partial results of the rows whose
  * tokens are shared out over several CTAs.  It depends on head_dim and on whether
  * a kv head has more than 48 rows (max_new * Hq / Hkv; bf16, without lists): 1.4 or 22 MB
- * at d = 64, 2.7 or 43 MB at d = 128, and not on the batch.  0 when p is invalid. */
+ * at d = 64, 2.7 or 43 MB at d = 128, and not on the batch.  0 when p is invalid,
+ * and when few rows see at most 128 tokens (max_pages * page_size, or max_blocks *
+ * block_size): the call then takes workspace NULL. */
 size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
 
 /*

@@ -126,6 +126,14 @@ def test_nothing_to_do_enqueues_nothing(kv4):
         assert _attend(kv4, p, q=None, o=None, ws=None, ws_bytes=0) == 0
 
 
+def test_workspace_is_needed_where_tokens_can_be_shared_out(kv4):
+    for change, none in ((dict(max_pages=2), True), (dict(max_pages=3), False),
+                         (dict(max_pages=2, max_new=13), False),              # 52 rows of a kv head
+                         (dict(list_heads=2, block_size=64, max_blocks=2), True),
+                         (dict(list_heads=2, block_size=64, max_blocks=3), False)):
+        assert (kv4.attend_workspace_bytes(_params(kv4, **change)) == 0) == none
+
+
 def test_cache_bytes_and_params_layout(kv4):
     p = _params(kv4)
     assert kv4.lib.sbsa_kv4_cache_bytes(ctypes.byref(p)) == 10 * 2 * 2 * 64 * 80
@@ -697,7 +705,10 @@ def test_binding_refuses(kv4, cuda):
         lambda: kv4.attend(b.g_cache, q, t, lens, cu, 0),
         lambda: kv4.attend(b.g_cache, q, t, lens, cu, 2, out=q[:, :2]),
         lambda: kv4.attend(b.g_cache, q, t, lens, cu, 2, idx=torch.zeros(2, 2, 1, dtype=torch.int32, device="cuda")),
-        lambda: kv4.attend(b.g_cache, q, t, lens, cu, 2, workspace=torch.empty(8, dtype=torch.uint8, device="cuda")),
+        # (a table of 160 tokens, which needs a workspace)
+        lambda: kv4.attend(b.g_cache, q, t.repeat(1, 5)[:, :10].contiguous(), lens, cu, 2,
+                           workspace=torch.empty(8, dtype=torch.uint8, device="cuda")),
+        lambda: kv4.attend(b.g_cache, q, t, lens, cu, 2, workspace=torch.empty(8, device="cuda")),
     ]
     for i, call in enumerate(bad):
         with pytest.raises((ValueError, RuntimeError)):
