@@ -58,7 +58,8 @@ constexpr float kHead = 6.f, kLazy = 4.f;
 
 // 8 computing warps take the tiles of 16 TT tokens in turn; with two of them a
 // scheduler the latency of a tile's chain (levels, products, weights, products) is what
-// they wait for, so 8 rows take two tiles of 16 at once.  The copying warp and its
+// they wait for, so they take two tiles of 16 at once (one: 524288 tokens 185 us, two 153;
+// drafts 78 and 73).  The copying warp and its
 // three idle neighbours are a warpgroup whose registers the computing warps take
 // over: 256 * 224 + 128 * 56 = 384 * 168, what the block is launched with.
 constexpr int kWarps = 8;
@@ -67,7 +68,7 @@ constexpr int kRegs = 224, kRegsCopy = 56;
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kSub = NT == 1 ? 2 : 1;    // TT
+  static constexpr int kSub = 2;                  // TT
   static constexpr int kTile = 16 * kSub;         // tokens of a warp's step
   static constexpr int kTiles = kUnit / kTile;    // of a stage
   static constexpr int kRows = 8 * NT;
