@@ -440,8 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     int n = 0, item = 0;
     int ended[2] = {0, 0};  // by buffer: 1 + the item that ended with its last token tile, else 0
     int kh = 0, kph = 0;    // ring place and phase of the keys of tile n; the values' follow them
-    bool ok = true;
-    for (; w.more() && ok; w.next(p), ++item) {
+    // out: all 128 threads know of a failure, and leave together (none may be missing at a barrier)
+    bool ok = true, out = false;
+    for (; w.more() && !out; w.next(p), ++item) {
       const int begin = w.begin(), end = w.end();
       uint32_t ve = 47;  // the values' exponent so far (as bf16 holds it; at least 2^-80)
       if (tok < 4) nan_pos[(item & 3) * 4 + tok] = INT_MAX;
@@ -482,10 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           mx[(warp - 8) * 2] = ka;
           mx[(warp - 8) * 2 + 1] = va;
         }
-        if (bar_red_or(1, 128, !ok)) {
-          ok = false;
-          break;
-        }
+        out = bar_red_or(1, 128, !ok);
+        if (out) break;
         ka = max(max(mx[0], mx[2]), max(mx[4], mx[6]));
         va = max(max(mx[1], mx[3]), max(mx[5], mx[7]));
         const uint32_t ke = max(ka >> 7, 47u);
@@ -574,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         kph = vh + 1 == kHalves ? vph ^ 1 : vph;
       }
     }
-    if (!ok && lane == 0 && !*abort_flag) fail();
+    if ((!ok || out) && lane == 0 && !*abort_flag) fail();
   } else {
     regs_lower<kRegsIssue>();
     if (warp == 12 && lane == 0) {
