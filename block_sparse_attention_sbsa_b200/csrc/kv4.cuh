@@ -53,13 +53,14 @@ __device__ __forceinline__ bool kv4_place(const Kv4Batch& b, int t, bool* in_seq
     kv4_record(b.status);
     return false;
   }
-  const int pg = b.table[(long long)s * b.max_pages + (int)(pos / b.page)];
+  const int page_log = __ffs(b.page) - 1;  // a power of two
+  const int pg = b.table[(long long)s * b.max_pages + ((int)pos >> page_log)];
   if (pg < 0 || pg >= b.n_pages) {
     kv4_record(b.status);
     return false;
   }
   *page = pg;
-  *off = (int)(pos % b.page);
+  *off = (int)pos & (b.page - 1);
   return true;
 }
 

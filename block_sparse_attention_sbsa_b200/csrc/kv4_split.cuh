@@ -120,16 +120,17 @@ __device__ __forceinline__ Seq seq_of(const SplitParams& p, int b) {
 
 // Row `row` of the item head: the token row, its number in the sequence and the
 // query head; false past the last.
-__device__ __forceinline__ bool row_of(const SplitParams& p, const Seq& s, int head, long long row,
+__device__ __forceinline__ bool row_of(const SplitParams& p, const Seq& s, int head, uint32_t row,
                                        long long* t, int* h, int* i) {
-  *i = (int)(row / p.group);
-  if (*i >= s.rows) return false;
-  *t = s.first + *i;
-  *h = head * p.group + (int)(row % p.group);
+  const uint32_t group = p.group, n = row / group;
+  *i = (int)n;
+  if (n >= (uint32_t)s.rows) return false;
+  *t = s.first + (int)n;
+  *h = head * p.group + (int)(row - n * group);
   return true;
 }
 
-// The items of one (sequence, head).
+// The items of one (sequence, head).  (Rows times heads fit 31 bits: checked on the host.)
 template <int ROWS>
 struct Items {
   Seq seq;
@@ -139,7 +140,7 @@ struct Items {
   __device__ Items() {}
   __device__ Items(const SplitParams& p, int b, int head) {
     seq = seq_of(p, b);
-    tiles = (int)(((long long)seq.rows * p.group + ROWS - 1) / ROWS);
+    tiles = (int)(((uint32_t)seq.rows * (uint32_t)p.group + ROWS - 1) / ROWS);
     listed = -1;
     if (p.a.list_heads) {
       const int n = clamp_int(p.a.cnt[(long long)b * p.heads + head], 0, p.a.max_blocks);
@@ -148,8 +149,8 @@ struct Items {
   }
   // Tokens that the tile's last row sees.
   __device__ int limit(const SplitParams& p, int tile) const {
-    const long long rows = min((long long)(tile + 1) * ROWS, (long long)seq.rows * p.group);
-    return max(0, seq.len - seq.rows + (int)((rows - 1) / p.group) + 1);
+    const uint32_t rows = min((uint32_t)(tile + 1) * ROWS, (uint32_t)seq.rows * (uint32_t)p.group);
+    return max(0, seq.len - seq.rows + (int)((rows - 1) / (uint32_t)p.group) + 1);
   }
   // Units of a tile; one that sees nothing still takes one (it writes zeros).
   __device__ int units(const SplitParams& p, int tile) const {
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const __grid_con
   const Seq s = seq_of(p, part.seq);
   long long t;
   int h, i;
-  if (!row_of(p, s, part.head, (long long)part.tile * ROWS + row, &t, &h, &i)) return;
+  if (!row_of(p, s, part.head, (uint32_t)part.tile * ROWS + row, &t, &h, &i)) return;
   auto slot = [&](int k) {
     return p.slots + (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) *
                          slot_floats(ROWS, D);
