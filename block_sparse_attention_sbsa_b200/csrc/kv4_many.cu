@@ -13,9 +13,14 @@
 //
 // Bound: the tensor cores and the exponentials alike.  A tile of 128 tokens against 256
 // rows is 2 * 2 * 2^21 multiply-adds, 2096 cycles at 4000 a cycle, its 2^15 exponentials
-// 2048 cycles at 16 a cycle; unpacking takes about 450 instructions a dequantising warp.  Neither
-// is reached: 4096 new of 32768 tokens, 32 query heads on 8, 2.68 ms (769 TFLOP/s, 0.46 of cuBLAS),
-// about 5,800 cycles a token tile, 5,200 of them of the unpacking warps' work.
+// 2048 cycles at 16 a cycle.  Neither is reached: 4096 new of 32768 tokens, 32 query heads on 8,
+// 2.02 ms (1020 TFLOP/s, 0.62 of cuBLAS), about 4,400 cycles a token tile: softmax 2,700 of them and
+// 1,500 of waiting for the products, unpacking 3,300 and 1,100 of waiting.
+// Four roles at a time share the instruction caches, so their loops are kept short (unroll 1 where
+// it stands): all unrolled, every role waited for instructions (2.5 warps of 4.3 a scheduler) and
+// the same call took 2.78 ms; with the unpacking loops short 2.25.  The softmax reads S twice
+// out of TMEM, 64 columns at a time, for the same reason, and then needs so few registers
+// that nobody spills (2.02).
 //
 // One CTA an SM, 16 warps:
 //   0-3, 4-7  softmax of tile A, of tile B: a thread has a row; S out of TMEM, P (fp16)
@@ -48,8 +53,8 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kRows = 256;  // of an item: two tiles of 128
 constexpr int kItemCost = 5;
 constexpr int kThreads = 512;
-// 256 * 184 + 128 * 80 + 128 * 64 = 512 * 128, what the block is launched with
-constexpr int kRegsSoftmax = 184, kRegsUnpack = 80, kRegsIssue = 64;
+// 256 * 152 + 128 * 128 + 128 * 80 = 512 * 128, what the block is launched with
+constexpr int kRegsSoftmax = 152, kRegsUnpack = 128, kRegsIssue = 80;
 constexpr float kRescaleLog2 = 8.0f;
 
 constexpr int kHalves = 3;
@@ -286,30 +291,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         const Info& in = info[n & 3];
         const float c = f * in.k_unit;
         const int ve = in.v_exp;
-        float s[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tmem_ld32(s_col + k * 32, *reinterpret_cast<float(*)[32]>(s + k * 32));
-        tmem_wait_ld();
         const uint32_t on = in.on[0] & in.on[1] & in.on[2] & in.on[3];
-        if (__any_sync(0xFFFFFFFFu, j * 128 + 128 > lim) || on != 0xFFFFFFFFu) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int left = lim - j * 128 - k * 32;  // of these 32 tokens the row sees so many
-            uint32_t bits = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
-            bits &= in.on[k];
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!((bits >> y) & 1u)) s[k * 32 + y] = -INFINITY;
-          }
-        }
+        const bool mask = __any_sync(0xFFFFFFFFu, j * 128 + 128 > lim) || on != 0xFFFFFFFFu;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // the maximum (a masked S goes back into TMEM)
+#pragma unroll 1
+        for (int k = 0; k < 128; k += 64) {
+          float s[64];
 #pragma unroll
-        for (int k = 0; k < 128; k += 4) {
-          mx[0] = fmaxf(mx[0], s[k]);
-          mx[1] = fmaxf(mx[1], s[k + 1]);
-          mx[2] = fmaxf(mx[2], s[k + 2]);
-          mx[3] = fmaxf(mx[3], s[k + 3]);
+          for (int y = 0; y < 64; y += 32)
+            tmem_ld32(s_col + k + y, *reinterpret_cast<float(*)[32]>(s + y));
+          tmem_wait_ld();
+          if (mask) {
+#pragma unroll
+            for (int z = 0; z < 64; z += 32) {
+              const int left = lim - j * 128 - k - z;  // of these 32 tokens the row sees so many
+              uint32_t bits = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1u;
+              bits &= in.on[(k + z) >> 5];
+#pragma unroll
+              for (int y = 0; y < 32; ++y)
+                if (!((bits >> y) & 1u)) s[z + y] = -INFINITY;
+            }
+#pragma unroll
+            for (int y = 0; y < 64; y += 16)
+              tmem_st16(s_col + k + y, *reinterpret_cast<float(*)[16]>(s + y));
+            tmem_wait_st();
+          }
+#pragma unroll
+          for (int y = 0; y < 64; y += 4) {
+            mx[0] = fmaxf(mx[0], s[y]);
+            mx[1] = fmaxf(mx[1], s[y + 1]);
+            mx[2] = fmaxf(mx[2], s[y + 2]);
+            mx[3] = fmaxf(mx[3], s[y + 3]);
+          }
         }
         const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c);
         if (j == begin) {
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           m = mn;
           const float ao = alpha * exp2f((float)(v_exp - ve));
           v_exp = ve;
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < D; k += 16) {
             float o[16];
             tmem_ld16(o_col + k, o);
@@ -335,31 +349,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         // (two at a time: packed fp32 operations halve what is issued for all but the exponentials)
         const uint64_t c2 = pack2(c, c), m2 = pack2(-m, -m);
         uint64_t sum = pack2(0.f, 0.f);
+        // the weights; PV of the first 64 tokens may begin while the others are at work
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float s[64];
+          tmem_ld32(s_col + half * 64, *reinterpret_cast<float(*)[32]>(s));
+          tmem_ld32(s_col + half * 64 + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t pk[16];
+          for (int k = 0; k < 2; ++k) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            float p0, p1;
-            unpack2(fma2(pack2(s[k * 32 + y], s[k * 32 + y + 1]), c2, m2), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            sum = add2(sum, pack2(p0, p1));
-            pk[y >> 1] = h2(__floats2half2_rn(p0, p1));
+            for (int y = 0; y < 32; y += 2) {
+              float p0, p1;
+              unpack2(fma2(pack2(s[k * 32 + y], s[k * 32 + y + 1]), c2, m2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              sum = add2(sum, pack2(p0, p1));
+              pk[y >> 1] = h2(__floats2half2_rn(p0, p1));
+            }
+            tmem_st16u(s_col + half * 32 + k * 16, pk);
           }
-          tmem_st16u(s_col + k * 16, pk);
-          if (k == 1) {  // PV of the first 64 tokens may begin
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&p_half[x]);
-          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(half ? &p_full[x] : &p_half[x]);
         }
         float sum0, sum1;
         unpack2(sum, sum0, sum1);
         l += sum0 + sum1;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
       // ---- O
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       const float u0 = exp2f((float)(v_exp >> 1)), u1 = exp2f((float)(v_exp - (v_exp >> 1)));
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.o) + t * p.a.o_token + h * p.a.o_head;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         float o[32];
         tmem_ld32(o_col + k, o);
@@ -428,14 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     const int off = tok & (page - 1);
     const int turn = NG == 4 ? ((off >> 1) & 1) * 2 : 0;  // pieces of a value's row change places
     // With 4 pieces neighbouring pairs of tokens begin at different ones, so that no bank is met
-    // twice.  Piece `piece[i]`'s words are chunks 4 piece to 4 piece + 3 of the token's row, at
-    // at[i] + word[k] (chunk_at).
-    int piece[kWords], at[kWords], word[4];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      piece[i] = NG == 4 ? (i + (tok >> 1)) & 3 : i;
-      at[i] = (piece[i] >> 1) * (128 * 128) + ((((piece[i] & 1) << 2) ^ (tok & 4)) << 4);
-    }
+    // twice.  A piece's words are chunks 4 piece to 4 piece + 3 of the token's row, at
+    // place(piece) + word[k] (chunk_at).
+    const int first = NG == 4 ? (tok >> 1) & 3 : 0;
+    auto place = [&](int piece) {
+      return (piece >> 1) * (128 * 128) + ((((piece & 1) << 2) ^ (tok & 4)) << 4);
+    };
+    int word[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) word[k] = tok * 128 + ((k ^ (tok & 3)) << 4);
     const unsigned char* ring = smem + C::kOffRing + (tok >> page_log) * rec;
@@ -516,13 +532,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
             so[g] = __float2half2_rn(sc * 0.0625f);
             lo[g] = __float2half2_rn(lw);
           }
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < kWords; ++i) {  // d = 128: piece q, words g; d = 64: two pieces of two
-            const uint4 u = reinterpret_cast<const uint4*>(kc + off * (D / 2))[piece[i]];
+            const int piece = (i + first) & (kWords - 1);
+            const uint4 u = reinterpret_cast<const uint4*>(kc + off * (D / 2))[piece];
             const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(dst + at[i] + word[k]) =
+              *reinterpret_cast<uint4*>(dst + place(piece) + word[k]) =
                   unpack8(wd[k], se[k % NG], so[k % NG], lo[k % NG]);
           }
           mbar_arrive(&c_free[kh]);
@@ -557,13 +574,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
             so[g] = __floats2half2_rn(sc[2 * g] * 0.0625f, sc[2 * g + 1] * 0.0625f);
             lo[g] = __floats2half2_rn(lw[2 * g], lw[2 * g + 1]);
           }
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < kWords; ++i) {
-            const uint4 u = reinterpret_cast<const uint4*>(vc + off * (D / 2))[piece[i] ^ turn];
+            const int piece = (i + first) & (kWords - 1);
+            const uint4 u = reinterpret_cast<const uint4*>(vc + off * (D / 2))[piece ^ turn];
             const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(dst + at[i] + word[k]) =
+              *reinterpret_cast<uint4*>(dst + place(piece) + word[k]) =
                   unpack8(wd[k], se[k % (NG / 2)], so[k % (NG / 2)], lo[k % (NG / 2)]);
           }
           mbar_arrive(&c_free[vh]);
