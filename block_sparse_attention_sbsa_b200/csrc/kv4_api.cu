@@ -77,10 +77,12 @@ Kv4Batch batch(const sbsa_kv4_params* p, const int32_t* table, const int32_t* le
 }
 
 // Which kernel: the one for many rows reads the cache once for 256 rows, the other one for
-// 16, but spends less on what it reads.
+// 16, but spends less on what it reads, so that it takes up to two reads (d = 128) or three
+// (d = 64) to equal it.  12 sequences of 907 to 20011 tokens, 8 kv heads, d = 128: 32 rows few
+// 82 us, many 109; 33 to 48 rows 115 and 109.  d = 64: 33 to 48 rows 81 and 92.
 bool many_rows(const sbsa_kv4_params* p) {
   return p->dtype == SBSA_BF16 && !p->list_heads &&
-         (long long)p->max_new * (p->n_q_heads / p->n_kv_heads) > 48;
+         (long long)p->max_new * (p->n_q_heads / p->n_kv_heads) > (p->head_dim == 64 ? 48 : 32);
 }
 
 // The sizes that the launchers go by (no pointers).

@@ -519,8 +519,8 @@ int sbsa_kv4_read(const sbsa_kv4_params* p, const void* cache, const int32_t* pa
 
 /* Device workspace of sbsa_kv4_attend: partial results of the rows whose
  * tokens are shared out over several CTAs.  It depends on head_dim and on whether
- * a kv head has more than 48 rows (max_new * Hq / Hkv; bf16, without lists): 1.4 or 22 MB
- * at d = 64, 2.7 or 43 MB at d = 128, and not on the batch.  0 when p is invalid,
+ * a kv head has more than 48 (d = 64) or 32 (d = 128) rows (max_new * Hq / Hkv; bf16, without
+ * lists): 1.4 or 22 MB at d = 64, 2.7 or 43 MB at d = 128, and not on the batch.  0 when p is invalid,
  * and when few rows see at most 128 tokens (max_pages * page_size, or max_blocks *
  * block_size): the call then takes workspace NULL. */
 size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
@@ -544,8 +544,8 @@ size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
  * repeated block is attended twice.
  * Precision: products in fp16 with fp32 accumulation, exact up to the rounding of the
  * weights (2^-11 of each; fp32 rows take both operands in two parts, 2^-22) and, for
- * more than 48 rows of a kv head, of the dequantised keys and values (2^-11).  Results
- * do not change between runs.
+ * more than 48 (d = 64) or 32 (d = 128) rows of a kv head, of the dequantised keys and values
+ * (2^-11).  Results do not change between runs.
  * Errors as sbsa_kv4_append, SBSA_ERR_UNSUPPORTED also for n_tokens * Hq or n_seqs * Hq
  * above 2^31 - 2^16, and SBSA_ERR_WORKSPACE for a missing, misaligned or short
  * workspace.
