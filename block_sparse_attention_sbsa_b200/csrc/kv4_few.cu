@@ -13,7 +13,7 @@
 // Bound: HBM, 5/4 d bytes a token and kv head.  At 6.5 TB/s an SM has about
 // 110 cycles for 16 tokens (d = 128, 2560 bytes), and the work on them is
 // about 350 warp instructions (88 issue cycles) at 8 rows and takes 150 cycles (524288 tokens of 8
-// kv heads, 64 query heads: 159 us, 4.2 TB/s; without the arithmetic 122): levels must be
+// kv heads, 64 query heads: 153 us, 4.4 TB/s; without the arithmetic 122): levels must be
 // unpacked with next to nothing, which rules out a copy in fp16 through shared
 // memory for tcgen05 (its writes and reads alone would exceed the shared memory's
 // bandwidth).  The products therefore run on mma.sync m16n8k16, whose
@@ -31,7 +31,7 @@
 // workspace, and the one that has its last unit joins them when it is done with its own
 // run: it waits only for CTAs before it, which wait for nobody before they have left their
 // parts.  (A second kernel for the joins cost a launch on the host, and on the GPU: 33 listed
-// blocks of 8 sequences 24.6 us, 23.0 without; 524288 tokens 164, 159.)  Everything is in
+// blocks of 8 sequences 24.6 us, 23.0 without; 524288 tokens 164, 159 at the time.)  Everything is in
 // a fixed order: results do not change between runs.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
