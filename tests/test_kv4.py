@@ -377,6 +377,23 @@ def test_attend_many_items_a_cta(kv4, cuda, d, most):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("most", [8, 9, 12, 13, 32, 33])
+def test_attend_at_the_limits_between_kernels(kv4, cuda, d, most):
+    """32, 36, 48 and 52 rows of a kv head (the kernels change after 32 or 48), 128 and 132 (one query tile
+    and two), with contexts that end at, before and behind a tile of 128 tokens."""
+    rng = np.random.default_rng(most + d)
+    lens = [128 + most, 127, 129, 640, 33, 1411]
+    new = [most, most, 1, most - 1, min(most, 33), most]
+    b = _fast_fill(Batch(lens, new, 32, 2, d, seed=most), rng).gpu()
+    q = _rows(rng, 8, b.total, d, "bf16", True, 1.5)
+    out = torch.zeros_like(q)
+    kv4.attend(b.g_cache, q, *b.g, most, out=out)
+    assert _status(kv4) == 0
+    _check(kv4, b, q, out, torch.zeros_like(out))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("list_heads", ["kv", "q"])
 @pytest.mark.parametrize("block,page,d,dtype", [(64, 64, 128, "bf16"), (128, 16, 64, "fp32"), (128, 128, 128, "bf16"),
                                                 (64, 32, 64, "bf16")])
@@ -561,6 +578,35 @@ def test_attend_spread_of_magnitudes(kv4, cuda, new):
     fin = np.r_[0:32, 64:128]
     tol = _tolerance(want, size, np.nan_to_num(span, nan=512.0), "bf16", n, d)
     assert (np.abs(out.float().cpu().numpy() - want)[..., fin] <= np.maximum(tol, 0.02)[..., fin] + 2.0 ** -7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,dtype", [(3, "bf16"), (3, "fp32"), (70, "bf16")])
+def test_attend_a_nan_key_is_met_only_by_rows_that_see_it(kv4, cuda, d, new, dtype):
+    """A key with a NaN in one group, among the new tokens: the rows before it stay what they are, the
+    others are NaN; so do the value's channels of its group alone with a NaN value."""
+    rng = np.random.default_rng(new + d)
+    n, at = 300, 300 - new + new // 2
+    b = _fast_fill(Batch([n], [new], 64, 1, d, seed=8), rng)
+    q = _rows(rng, 4, new, d, dtype, True, 1.2)
+    want, size, span = KP.attend(KP.decode(b.cache), q.float().cpu().numpy(), b.table, b.lens, b.cu)
+    tol = _tolerance(want, size, span, dtype, n, d)
+    first = at - (n - new)  # the first row that sees it
+    for side in (0, 1):
+        kept = b.cache.copy()
+        x = rng.standard_normal((2, 1, d)).astype(np.float32)
+        x[side, 0, 33] = np.nan
+        b.put(0, at, x[0], x[1])
+        b.gpu()
+        out = torch.zeros(4, new, d, dtype=DT[dtype], device="cuda")
+        kv4.attend(b.g_cache, q, *b.g, new, out=out)
+        got = out.float().cpu().numpy()
+        assert (np.abs(got - want)[:, :first] <= tol[:, :first]).all()
+        assert np.isnan(got[:, first:, slice(None) if side == 0 else slice(32, 64)]).all()
+        if side:
+            assert np.isfinite(np.delete(got[:, first:], np.r_[32:64], axis=2)).all()
+        b.cache[...] = kept
 
 
 @pytest.mark.gpu
