@@ -60,6 +60,7 @@ constexpr int kThreads = 512;
 // 256 * 152 + 128 * 128 + 128 * 80 = 512 * 128, what the block is launched with
 constexpr int kRegsSoftmax = 152, kRegsUnpack = 128, kRegsIssue = 80;
 constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLeastFactor = 0x1p-126f, kMostFactor = 0x1p80f;  // (|S'| is below 2^32)
 
 constexpr int kHalves = 3;
 
@@ -93,10 +94,10 @@ struct MC {
 
 // What the softmax has to know of a tile of tokens.
 struct Info {
-  float k_unit;      // logits are S' * k_unit (a power of two) * the row's factor
+  float k_unit[2];   // logits are S' * both (powers of two) * the row's factor
   int v_exp;         // O's unit after this tile: 2^v_exp
   uint32_t on[4];    // tokens whose page is in the cache
-  int pad[2];
+  int pad;
 };
 static_assert(sizeof(Info) == 32, "Info");
 
@@ -293,7 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         const Info& in = info[n & 3];
-        const float c = f * in.k_unit;
+        // A zero row's f and a tile of zero keys make a c below fp32's least value, and -inf * 0, a masked
+        // score's, would be NaN: c stays positive (S' is 0 there or the logit next to it) and finite.
+        const float c = fminf(fmaxf(f * in.k_unit[0] * in.k_unit[1], kLeastFactor), kMostFactor);
         const int ve = in.v_exp;
         const uint32_t on = in.on[0] & in.on[1] & in.on[2] & in.on[3];
         const bool mask = __any_sync(0xFFFFFFFFu, j * 128 + 128 > lim) || on != 0xFFFFFFFFu;
@@ -520,7 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         if (ok) {
           Info& in = info[n & 3];
           if (tok == 0) {
-            in.k_unit = exp2f((float)kn);
+            // in two factors: 2^kn alone, or with a small f, may leave fp32's range
+            in.k_unit[0] = exp2f((float)(kn >> 1));
+            in.k_unit[1] = exp2f((float)(kn - (kn >> 1)));
             in.v_exp = vn;
           }
           if (lane == 0) in.on[warp - 8] = on;

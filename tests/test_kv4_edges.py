@@ -1,0 +1,102 @@
+"""The 4-bit key-value cache where its operators are easily wrong: zero rows and zero keys, lengths and
+rows beyond what a table or a tensor holds, groups of different magnitude, weights far below the
+largest, replays of captured graphs.  Tolerances as in test_kv4.py, plus what stands at a test.
+"""
+import numpy as np
+import pytest
+import torch
+
+import kv4_plain as KP
+from test_kv4 import DT, Batch, _check, _fast_fill, _rows, _status, _tolerance, kv4  # noqa: F401
+
+
+def _token(b, seq, pos, side, head):
+    """The levels' bytes and the pairs (uint16 [d / 32, 2]: scale, low) of one key (side 0) or value of the
+    host's cache, as views."""
+    off, d = pos % b.page, b.d
+    rec = b.cache[b.table[seq, pos // b.page], head, side].reshape(-1)
+    at = b.page * d // 2 + off * d // 8
+    return rec[off * d // 2:(off + 1) * d // 2], rec[at:at + d // 8].view(np.uint16).reshape(-1, 2)
+
+
+def _constant(b, seq, pos, side, value):
+    """The key or value of a token at all heads: constant groups of a value that bf16 holds."""
+    bits = np.float32(value).view(np.uint32)
+    assert bits & 0xFFFF == 0
+    for h in range(b.hkv):
+        levels, pairs = _token(b, seq, pos, side, h)
+        levels[:], pairs[:, 0], pairs[:, 1] = 0, 0, bits >> 16
+
+
+# -------------------------------------------------------------------------- zero rows, zero and huge keys
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 33, 49, 300])
+def test_zero_rows_and_zero_keys(kv4, cuda, d, new):
+    """A chunk of zeros over zero keys, zeros behind a prompt (a tile of 128 and more), zero rows over keys
+    and rows over zero keys: few rows, and many with one and with two query tiles."""
+    rng = np.random.default_rng(new + d)
+    lens = [new, 700, 400, 450]
+    b = _fast_fill(Batch(lens, [min(new, n) for n in lens], 32, 2, d, seed=new), rng)
+    for s, first in ((0, 0), (1, 250), (3, 0)):
+        for pos in range(first, lens[s]):
+            _constant(b, s, pos, 0, 0.0)
+    b.gpu()
+    q = _rows(rng, 2, b.total, d, "bf16", True, 1.5)
+    q[:, :b.cu[3]] = 0
+    out = torch.full_like(q, 3.0)
+    kv4.attend(b.g_cache, q, *b.g, new, out=out)
+    assert _status(kv4) == 0
+    _check(kv4, b, q, out, out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 33, 300])
+def test_a_dry_run_of_zeros(kv4, cuda, d, new):
+    """Zeros over a cache of zeros are zeros; rows before the first token too, which are reported."""
+    cache = kv4.empty(12, 2, 64, d)
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(2, 6)
+    q = torch.zeros(8, 2 * new, d, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, new, 2 * new], dtype=torch.int32, device="cuda")
+    for short, status in ((new, 0), (new // 2, 6)):
+        lens = torch.tensor([300, short], dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, 3.0)
+        kv4.attend(cache, q, table, lens, cu, new, out=out)
+        assert _status(kv4) == status and (out == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [2, 33, 300])
+def test_zero_rows_over_pages_outside_the_cache(kv4, cuda, d, new):
+    """A tile of tokens whose pages all lie outside the cache: a zero row's weights are equal over the others."""
+    rng = np.random.default_rng(new)
+    n = 128 * 3 + new
+    b = _fast_fill(Batch([n], [new], 32, 1, d, seed=2), rng).gpu()
+    b.g[0][0, 4:8] = torch.tensor([b.pages, -1, b.pages + 9, -7], dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, new, d, dtype=torch.bfloat16, device="cuda")
+    out = kv4.attend(b.g_cache, q, *b.g, new).double().cpu().numpy()
+    assert _status(kv4) == 6
+    v = KP.tokens(KP.decode(b.cache), b.table[0], n)[1][:, 0].astype(np.float64)
+    v[128:256] = 0
+    want = np.cumsum(v, 0)[n - new:] / (np.arange(n - new, n) + 1 - 128)[:, None]
+    assert (np.abs(out - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * np.abs(v).max()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_near_the_end_of_the_range(kv4, cuda, d):
+    """Keys up to 2^121 against rows of 2^-122: ordinary logits (all of it powers of two, so exact)."""
+    rng = np.random.default_rng(d)
+    new, n = 70, 300
+    b = _fast_fill(Batch([n], [new], 32, 1, d, seed=3), rng)
+    for pos in range(n):
+        _constant(b, 0, pos, 0, float(rng.choice([-1, 1])) * 2.0 ** int(rng.integers(119, 122)))
+    b.gpu()
+    sign = torch.from_numpy(rng.choice([-1.0, 1.0], (2, new, 1))).cuda()
+    q = (sign * 2.0 ** -122).expand(2, new, d).to(torch.bfloat16).contiguous()
+    out = kv4.attend(b.g_cache, q, *b.g, new)
+    assert _status(kv4) == 0
+    _check(kv4, b, q, out, out)
