@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
       const int e = clamp_int(137 - (int)(__float_as_uint(mx) >> 23), -90, 100);
       const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-      const float fr = p.scale_log2 * __uint_as_float((uint32_t)(kUnitLog2 - e + 127) << 23);
+      // (positive: -inf * 0, a masked logit's, would be NaN)
+      const float fr = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(kUnitLog2 - e + 127) << 23), 0x1p-126f);
       // rows that see nothing (before the sequence, beyond max_new) mask all; rows past the
       // tile's last mask nothing, so that they never send the warp to the masked path
       int lr = INT_MAX;

@@ -100,3 +100,17 @@ def test_keys_near_the_end_of_the_range(kv4, cuda, d):
     out = kv4.attend(b.g_cache, q, *b.g, new)
     assert _status(kv4) == 0
     _check(kv4, b, q, out, out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,dtype", [(1, "bf16"), (1, "fp32"), (3, "bf16"), (3, "fp32"), (70, "bf16")])
+def test_zero_rows_at_a_tiny_logit_scale(kv4, cuda, new, dtype):
+    """Weights are equal then, for zero rows and for others."""
+    rng = np.random.default_rng(new)
+    b = _fast_fill(Batch([77 + new, 200], [new, new], 32, 2, 64, seed=6), rng).gpu()
+    q = _rows(rng, 4, b.total, 64, dtype, True)
+    q[:, ::2] = 0
+    for scale in (1e-30, 1e-38):
+        out = kv4.attend(b.g_cache, q, *b.g, new, sm_scale=scale)
+        assert _status(kv4) == 0
+        _check(kv4, b, q, out, out, scale=float(np.float32(scale)), dtype=dtype)
