@@ -17,9 +17,8 @@ __device__ __forceinline__ int clamp_int(int x, int lo, int hi) {
   return x < lo ? lo : (x > hi ? hi : x);
 }
 
-// Tokens of sequence b, within what its row of the page table can name.
-__device__ __forceinline__ int kv4_len(const Kv4Batch& b, int seq) {
-  const int n = b.lens[seq];
+// Tokens of a sequence whose length is given as n that its row of the page table can name.
+__device__ __forceinline__ int kv4_named(const Kv4Batch& b, int n) {
   const int c = clamp_int(n, 0, b.max_pages * b.page);
   if (c != n) kv4_record(b.status);
   return c;
@@ -47,9 +46,10 @@ __device__ __forceinline__ bool kv4_place(const Kv4Batch& b, int t, bool* in_seq
   const int s = kv4_seq_of(b, t);
   *in_seq = s >= 0;
   if (s < 0) return false;
-  const int len = kv4_len(b, s);
+  // positions go by the length as it is given, also where the table ends before it
+  const int len = b.lens[s];
   const long long pos = (long long)len - b.cu[s + 1] + t;
-  if (pos < 0 || pos >= len) {
+  if (pos < 0 || pos >= kv4_named(b, len)) {
     kv4_record(b.status);
     return false;
   }

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
     for (; w.more() && ok; w.next(p)) {
       const Seq s = w.seq;
       const int begin = w.begin(), end = w.end();
-      const int limit = w.limit();
+      const int limit = w.limit(), len = s.len(p);
       const int32_t* list = nullptr;
       int count = 0;
       if (p.a.list_heads) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
           const int e = (int)(at >> block_log);
           if (e >= count) return -1;
           const int j = list[e];
-          if (j < 0 || j > (s.len - 1) >> block_log || s.len == 0) {
+          if (j < 0 || j > (len - 1) >> block_log || len == 0) {
             kv4_record(p.a.b.status);
             return -1;
           }
@@ -418,13 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
       const float up = __uint_as_float((uint32_t)(e + 127) << 23);
       // (positive: -inf * 0, a masked logit's, would be NaN)
       const float fr = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(kUnitLog2 - e + 127) << 23), 0x1p-126f);
-      // rows that see nothing (before the sequence, beyond max_new) mask all; rows past the
+      // rows that see nothing (out of the sequence's range, beyond max_new) mask all; rows past the
       // tile's last mask nothing, so that they never send the warp to the masked path
       int lr = INT_MAX;
       if (have) {
-        const int visible = s.len - s.rows + i + 1;
-        lr = i < p.a.max_new ? max(visible, 0) : 0;
-        if ((visible < 1 || i >= p.a.max_new) && q == 0) kv4_record(p.a.b.status);
+        lr = i < p.a.max_new ? s.visible(p, i) : 0;
+        if (lr == 0 && q == 0) kv4_record(p.a.b.status);
         lim_min = min(lim_min, lr);
         lim_max = max(lim_max, lr);
       }

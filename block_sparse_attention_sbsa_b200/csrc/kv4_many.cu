@@ -241,11 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       int h = 0, i = 0;
       const bool have = row_of(p, w.seq, w.head, (uint32_t)w.tile * kRows + x * 128 + row, &t, &h, &i);
       // ---- Q: the row in fp16, scaled by a power of two to a largest element near 2^10
-      const int visible = w.seq.len - w.seq.rows + i + 1;
       int lim = w.limit();  // rows past the last see all, so that they never mask
       if (have) {
-        lim = i < p.a.max_new ? max(visible, 0) : 0;
-        if (visible < 1 || i >= p.a.max_new) kv4_record(p.a.b.status);
+        lim = i < p.a.max_new ? w.seq.visible(p, i) : 0;
+        if (lim == 0) kv4_record(p.a.b.status);
       }
       float f;
       {

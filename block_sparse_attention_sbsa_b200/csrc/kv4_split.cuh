@@ -45,6 +45,7 @@ struct SplitParams {
   int heads;         // items per sequence and row tile: kv heads, or listed query heads
   int group;         // query heads of an item
   int kv_div;        // item head / kv_div = kv head
+  int capacity;      // tokens that a row of the page table can name
   float scale_log2;  // sm_scale * log2(e)
   float* slots;      // two a CTA: of the item that begins before its run, and of the one that
                      // goes on behind it
@@ -70,6 +71,7 @@ inline SplitParams split_params(const Kv4AttendArgs& a, int slot_rows) {
   p.heads = a.list_heads ? a.list_heads : a.b.hkv;
   p.group = a.hq / p.heads;
   p.kv_div = p.heads / a.b.hkv;
+  p.capacity = a.b.max_pages * a.b.page;  // below 2^31 - 2^16: checked with the parameters
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   p.slots = static_cast<float*>(a.workspace);
   p.parts = reinterpret_cast<Part*>(p.slots + kMaxCtas * 2 * slot_floats(slot_rows, a.d));
@@ -103,9 +105,19 @@ inline bool split_possible(const Kv4AttendArgs& a) {
   return (long long)a.b.max_pages * a.b.page > kSplitUnit;
 }
 
-// A sequence as an item sees it.
+// A sequence as an item sees it: its first row and number of rows, and the first row's position.
+// (The position of a row fits 31 bits; 1 more than it are the tokens that the row sees.)
 struct Seq {
-  int first, rows, len;  // first row, number of rows, tokens
+  int first, rows, ahead;
+
+  // Tokens that row i sees: 0 before the sequence's first token and behind the last one that the
+  // table can name.
+  __device__ int visible(const SplitParams& p, int i) const {
+    const int n = ahead + i + 1;
+    return n < 1 || n > p.capacity ? 0 : n;
+  }
+  // Tokens of the sequence, as far as the table can name them.
+  __device__ int len(const SplitParams& p) const { return clamp_int(ahead + rows, 0, p.capacity); }
 };
 
 __device__ __forceinline__ Seq seq_of(const SplitParams& p, int b) {
@@ -114,7 +126,9 @@ __device__ __forceinline__ Seq seq_of(const SplitParams& p, int b) {
   const int hi = clamp_int(p.a.b.cu[b + 1], lo, p.a.b.n_tokens);
   s.first = lo;
   s.rows = hi - lo;
-  s.len = kv4_len(p.a.b, b);
+  const int len = p.a.b.lens[b];
+  kv4_named(p.a.b, len);
+  s.ahead = (int)max((long long)len - s.rows, -0x7FFF0000LL);
   return s;
 }
 
@@ -147,10 +161,10 @@ struct Items {
       listed = (n * p.a.block + kSplitUnit - 1) / kSplitUnit;
     }
   }
-  // Tokens that the tile's last row sees.
+  // Tokens that no row of the tile sees more of: those of its last row, as far as there are any.
   __device__ int limit(const SplitParams& p, int tile) const {
     const uint32_t rows = min((uint32_t)(tile + 1) * ROWS, (uint32_t)seq.rows * (uint32_t)p.group);
-    return max(0, seq.len - seq.rows + (int)((rows - 1) / (uint32_t)p.group) + 1);
+    return clamp_int(seq.ahead + (int)((rows - 1) / (uint32_t)p.group) + 1, 0, p.capacity);
   }
   // Units of a tile; one that sees nothing still takes one (it writes zeros).
   __device__ int units(const SplitParams& p, int tile) const {

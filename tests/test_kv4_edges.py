@@ -114,3 +114,49 @@ def test_zero_rows_at_a_tiny_logit_scale(kv4, cuda, new, dtype):
         out = kv4.attend(b.g_cache, q, *b.g, new, sm_scale=scale)
         assert _status(kv4) == 0
         _check(kv4, b, q, out, out, scale=float(np.float32(scale)), dtype=dtype)
+
+
+# ---------------------------------------------------------------- lengths and rows beyond what is there
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,over", [(1, 1), (4, 3), (4, 6), (70, 9)])
+def test_a_length_beyond_the_table(kv4, cuda, d, new, over):
+    """The rows whose tokens the table cannot name are skipped and reported; the others are the tokens that
+    they are, and no other token of the cache is touched."""
+    rng = np.random.default_rng(new + over)
+    page, hkv, hq, n = 16, 2, 4, 160
+    b = _fast_fill(Batch([n, 45], [new, min(new, 45)], page, hkv, d, seed=4), rng).gpu()
+    table = b.g[0][:, :n // page].contiguous()
+    lens = b.g[1].clone()
+    lens[0] = n + over
+    have = max(0, new - over)                                        # rows of sequence 0 with a place
+    k, v = (_rows(rng, hkv, b.total, d, "bf16", True) for _ in range(2))
+    ks, vs = (torch.full((hkv, b.total, d), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kv4.append(b.g_cache, k, v, table, lens, b.g[2], k_stored=ks, v_stored=vs)
+    assert _status(kv4) == 6
+    xk, xv = k.float().cpu().numpy(), v.float().cpu().numpy()
+    for t in range(have):
+        b.put(0, n + over - new + t, xk[:, t], xv[:, t])
+    for t in range(new, b.total):
+        b.put(1, 45 - b.total + t, xk[:, t], xv[:, t])
+    assert np.array_equal(b.g_cache.cpu().numpy(), b.cache)
+    assert (ks[:, have:new] == 9).all() and (vs[:, have:new] == 9).all()
+    ko, vo = (torch.full_like(ks, 9.0) for _ in range(2))
+    kv4.read(b.g_cache, table, lens, b.g[2], k_out=ko, v_out=vo)
+    assert _status(kv4) == 6
+    for got, want in ((ko, ks), (vo, vs)):
+        assert (got[:, have:new] == 0).all()
+        assert torch.equal(got[:, :have], want[:, :have]) and torch.equal(got[:, new:], want[:, new:])
+    q = _rows(rng, hq, b.total, d, "bf16", True, 1.5)
+    out = torch.full_like(q, 3.0)
+    kv4.attend(b.g_cache, q, table, lens, b.g[2], new, out=out)
+    assert _status(kv4) == 6 and (out[:, have:new] == 0).all()
+    decoded = KP.decode(b.cache)
+    for s, rows, at in ((0, range(have), n + over - new), (1, range(new, b.total), 45 - b.total)):
+        for t in rows:                                                # one row at a time: its tokens end at its own
+            pos = at + t
+            want, size, span = KP.attend(decoded, q[:, t:t + 1].float().cpu().numpy(), b.table[s:s + 1],
+                                         [pos + 1], np.array([0, 1]))
+            err = np.abs(out[:, t:t + 1].float().cpu().numpy() - want)
+            assert (err <= _tolerance(want, size, span, "bf16", n, d)).all()
