@@ -38,6 +38,11 @@ __device__ __forceinline__ int kv4_seq_of(const Kv4Batch& b, int t) {
   return lo >= 1 && lo <= b.n_seqs ? lo - 1 : -1;
 }
 
+// Reports a batch that names rows before the tensors' first or behind their last.
+__device__ __forceinline__ void kv4_check_rows(const Kv4Batch& b) {
+  if (b.cu[0] < 0 || b.cu[b.n_seqs] > b.n_tokens) kv4_record(b.status);
+}
+
 // Page number and token of the page of row t; false (and recorded where it
 // is an error) when row t has no place in the cache.  *in_seq tells whether
 // the row belongs to a sequence at all.

@@ -173,6 +173,9 @@ struct Places {
 
 template <int TOKENS>
 __device__ __forceinline__ void find_places(const Kv4Batch& b, int t0, Places<TOKENS>& pl) {
+  // (a thread that looks up none)
+  if (threadIdx.x == kThreads - 1 && t0 == 0 && blockIdx.y == 0) kv4_check_rows(b);
+  static_assert(TOKENS < kThreads, "a thread to spare");
   for (int i = threadIdx.x; i < TOKENS; i += kThreads) {
     int page = -2, off = 0;
     if (t0 + i < b.n_tokens) {

@@ -122,13 +122,14 @@ struct Seq {
 
 __device__ __forceinline__ Seq seq_of(const SplitParams& p, int b) {
   Seq s;
-  const int lo = clamp_int(p.a.b.cu[b], 0, p.a.b.n_tokens);
-  const int hi = clamp_int(p.a.b.cu[b + 1], lo, p.a.b.n_tokens);
+  // the rows that the tensors have; positions go by cu and the length as they are given
+  const int from = p.a.b.cu[b], to = p.a.b.cu[b + 1], len = p.a.b.lens[b];
+  const int lo = clamp_int(from, 0, p.a.b.n_tokens), hi = clamp_int(to, lo, p.a.b.n_tokens);
+  if (lo != from || hi != to) kv4_record(p.a.b.status);
+  kv4_named(p.a.b, len);
   s.first = lo;
   s.rows = hi - lo;
-  const int len = p.a.b.lens[b];
-  kv4_named(p.a.b, len);
-  s.ahead = (int)max((long long)len - s.rows, -0x7FFF0000LL);
+  s.ahead = (int)max((long long)len - to + lo, -0x7FFF0000LL);
   return s;
 }
 

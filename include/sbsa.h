@@ -457,9 +457,9 @@ int sbsa_prefill_noalloc(const sbsa_params* p, const void* q, const void* k, con
  * None of it is read by the host: lengths and tables may change between the
  * replays of a captured graph.  What is out of range there (a page number
  * outside [0, n_pages), a negative length or one beyond the table, a row of a token
- * before the sequence's first or behind the table's last) is skipped as said at each
- * operator and reported as SBSA_ERR_DEVICE through sbsa_get_status; the other rows
- * keep their positions.
+ * before the sequence's first or behind the table's last, rows of cu_new before row 0 or
+ * behind row n_tokens - 1) is skipped as said at each operator and reported as
+ * SBSA_ERR_DEVICE through sbsa_get_status; the other rows keep their positions.
  * Pointers and strides belong to the current device.  n_seqs = 0 or
  * n_tokens = 0 enqueues nothing.
  */

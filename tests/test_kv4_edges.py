@@ -160,3 +160,39 @@ def test_a_length_beyond_the_table(kv4, cuda, d, new, over):
                                          [pos + 1], np.array([0, 1]))
             err = np.abs(out[:, t:t + 1].float().cpu().numpy() - want)
             assert (err <= _tolerance(want, size, span, "bf16", n, d)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [5, 70])
+@pytest.mark.parametrize("first,last", [(0, 2), (0, "new"), (-2, 0), (-2, 3)])
+def test_rows_that_the_tensors_do_not_have(kv4, cuda, new, first, last):
+    """cu_new names rows before the tensors' first or behind their last: the rows that are there are the tokens
+    that cu_new says, in all three operators, and the rest is reported."""
+    rng = np.random.default_rng(new + 10)
+    page, d, hkv, hq = 32, 64, 2, 4
+    b = _fast_fill(Batch([300, 90], [new, new], page, hkv, d, seed=7), rng).gpu()
+    lo, hi = -first, b.total - (new + 2 if last == "new" else last)      # rows of the whole batch that are there
+    cu = b.g[2] + first
+    k, v = (_rows(rng, hkv, b.total, d, "bf16", True) for _ in range(2))
+    kv4.append(b.g_cache, k[:, lo:hi], v[:, lo:hi], *b.g[:2], cu)
+    assert _status(kv4) == 6
+    xk, xv = k.float().cpu().numpy(), v.float().cpu().numpy()
+    for t in range(lo, hi):
+        s = int(t >= new)
+        b.put(s, b.lens[s] - b.cu[s + 1] + t, xk[:, t], xv[:, t])
+    assert np.array_equal(b.g_cache.cpu().numpy(), b.cache)
+    ko = torch.full((hkv, hi - lo, d), 9.0, dtype=torch.float32, device="cuda")
+    kv4.read(b.g_cache, *b.g[:2], cu, k_out=ko)
+    assert _status(kv4) == 6
+    decoded = KP.decode(b.cache)
+    for t in range(lo, hi):
+        s = int(t >= new)
+        pos = b.lens[s] - b.cu[s + 1] + t
+        assert np.array_equal(ko[:, t - lo].cpu().numpy(), KP.tokens(decoded, b.table[s], b.lens[s])[0][pos])
+    q = _rows(rng, hq, b.total, d, "bf16", True, 1.5)
+    out = torch.full((hi - lo, hq, d), 3.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    kv4.attend(b.g_cache, q[:, lo:hi], *b.g[:2], cu, new, out=out)
+    assert _status(kv4) == 6
+    want, size, span = KP.attend(decoded, q.float().cpu().numpy(), b.table, b.lens, b.cu)
+    err = np.abs(out.float().cpu().numpy() - want[:, lo:hi])
+    assert (err <= _tolerance(want, size, span, "bf16", 300, d)[:, lo:hi]).all()
