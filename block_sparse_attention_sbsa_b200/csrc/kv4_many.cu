@@ -4,12 +4,15 @@
 // Mathematics.  Keys and values are taken back to fp16 once a tile of 128 tokens
 // and used for 256 rows (two query tiles A and B of 128: tokens by query heads of a
 // kv head): S = Q K^T, exact online softmax, O += P V.  In fp16 a value stands for
-// (low' + scale' n), with low' and scale' scaled by a power of two common to the tile
-// so that both stay below 2^-8: a level in the low bits of a half is the fp16 denormal
+// (low' + scale' n), with low' and scale' scaled by a power of two so that scale' stays
+// below 2^-8 and low' below 2^14: a level in the low bits of a half is the fp16 denormal
 // n 2^-24, and one fused multiply-add by scale' 2^24 (2^20 where the level stands at bit
-// 4) gives the value, rounded once, 2^-11 of it (2^-21 of the tile's largest for those far
-// below).  q's rows are scaled to fp16 exactly.  The powers of two go into the logits'
-// factor and, for the values, into O's rescaling.
+// 4) gives the value, rounded once, 2^-11 of it.  Where low' or the value is an fp16
+// denormal itself, each is off by up to 2^-25, together 2^-15 of the largest scale that the
+// power of two goes by (or 2^-37 of the largest low, when that is above 2^22 scales): for keys
+// it is that of the tile's 128 tokens, all groups; for values each group has its own, the
+// largest of the item's tokens so far.  q's rows are scaled to fp16 exactly.  The powers of
+// two go into the logits' factor and, for the values, into the rescaling of O's columns.
 //
 // Bound: the tensor cores and the exponentials alike.  A tile of 128 tokens against 256
 // rows is 2 * 2 * 2^21 multiply-adds, 2096 cycles at 4000 a cycle, its 2^15 exponentials
@@ -95,11 +98,23 @@ struct MC {
 // What the softmax has to know of a tile of tokens.
 struct Info {
   float k_unit[2];   // logits are S' * both (powers of two) * the row's factor
-  int v_exp;         // O's unit after this tile: 2^v_exp
+  uint32_t v_exp;    // O's units after this tile: a byte e for each group, 2^(e - 118)
   uint32_t on[4];    // tokens whose page is in the cache
   int pad;
 };
 static_assert(sizeof(Info) == 32, "Info");
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// What a group's power of two has to reach: the larger of its scale and 2^-22 of its low, as bf16
+// holds it; 0 for a NaN group.
+__device__ __forceinline__ uint32_t reach(uint32_t pair) {
+  const int scale = pair & 0x7FFFu, low = (pair >> 16) & 0x7FFFu;
+  return scale >= 0x7F80 || low >= 0x7F80 ? 0u : (uint32_t)max(scale, low - (22 << 7));
+}
+// The power of two that byte g of v_exp stands for.
+__device__ __forceinline__ int unit_exp(uint32_t bytes, int g) {
+  return (int)((bytes >> (8 * g)) & 255u) - 118;
+}
 
 __device__ __forceinline__ uint32_t h2(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
@@ -139,6 +154,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // Offset of chunk c (8 elements) of row `row` in a tile of 128 rows.
 __device__ __forceinline__ int chunk_at(int row, int c) {
   return (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+// Group of place y of O (or k + y, k a multiple of 16).
+template <int NG>
+__device__ __forceinline__ constexpr int group_of(int y) {
+  return NG == 4 ? 2 * ((y >> 3) & 1) + (y & 1) : (y & 1);
 }
 
 template <int D>
@@ -287,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       mbar_arrive(&q_full[x]);
 
       float m = -FLT_MAX, l = 0.f;
-      int v_exp = INT_MIN;
+      uint32_t v_exp = 0;
       for (int j = begin; j < end; ++j, ++n) {
         ok = __all_sync(0xFFFFFFFFu, wait(&s_bar[x * 2 + (n & 1)], (n >> 1) & 1));
         if (!ok) break;
@@ -296,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         // A zero row's f and a tile of zero keys make a c below fp32's least value, and -inf * 0, a masked
         // score's, would be NaN: c stays positive (S' is 0 there or the logit next to it) and finite.
         const float c = fminf(fmaxf(f * in.k_unit[0] * in.k_unit[1], kLeastFactor), kMostFactor);
-        const int ve = in.v_exp;
+        const uint32_t ve = in.v_exp;
         const uint32_t on = in.on[0] & in.on[1] & in.on[2] & in.on[3];
         const bool mask = __any_sync(0xFFFFFFFFu, j * 128 + 128 > lim) || on != 0xFFFFFFFFu;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -340,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           const float alpha = exp2f(m - mn);
           l *= alpha;
           m = mn;
-          const float ao = alpha * exp2f((float)(v_exp - ve));
+          float ao[NG];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) ao[g] = alpha * exp2f((float)(unit_exp(v_exp, g) - unit_exp(ve, g)));
           v_exp = ve;
 #pragma unroll 1
           for (int k = 0; k < D; k += 16) {
@@ -348,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
             tmem_ld16(o_col + k, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] *= ao;
+            for (int y = 0; y < 16; ++y) o[y] *= ao[group_of<NG>(y)];
             tmem_st16(o_col + k, o);
           }
         }
@@ -393,9 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
       const int* np = nan_pos + (item & 3) * 4;
       float* slot = p.slots + (size_t)(2 * cta + (begin == 0 ? 1 : 0)) * slot_floats(kRows, D);
       const int sr = x * 128 + row;
-      // powers of two of the values' unit, in two steps (each within fp32's range)
-      const float u0 = exp2f((float)(v_exp >> 1)), u1 = exp2f((float)(v_exp - (v_exp >> 1)));
-      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      // 1 / l and the powers of two of the values' units, these in two steps (each within fp32's range)
+      float u0[NG], u1[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int e = unit_exp(v_exp, g);
+        u0[g] = pow2(e >> 1) * (whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+        u1[g] = pow2(e - (e >> 1));
+      }
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.o) + t * p.a.o_token + h * p.a.o_head;
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
@@ -404,9 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         tmem_wait_ld();
 #pragma unroll
         for (int y = 0; y < 32; ++y) {
-          // place k + y: group 2 (chunk & 1) + (y & 1) with 4 groups, y & 1 with 2
-          const int g = NG == 4 ? 2 * ((y >> 3) & 1) + (y & 1) : (y & 1);
-          o[y] = lim > np[g] ? NAN : o[y] * inv * u0 * u1;
+          const int g = group_of<NG>(y);
+          o[y] = lim > np[g] ? NAN : o[y] * u0[g] * u1[g];
         }
         if (!whole) {
 #pragma unroll
@@ -468,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
     bool ok = true, out = false;
     for (; w.more() && !out; w.next(p), ++item) {
       const int begin = w.begin(), end = w.end();
-      uint32_t ve = 47;  // the values' exponent so far (as bf16 holds it; at least 2^-80)
+      uint32_t ve = 0x2F2F2F2Fu;  // the values' units so far, a byte a group (at least 2^-80)
       if (tok < 4) nan_pos[(item & 3) * 4 + tok] = INT_MAX;
       for (int j = begin; j < end; ++j, ++n) {
         const int vh = kh + 1 == kHalves ? 0 : kh + 1, vph = kh + 1 == kHalves ? kph ^ 1 : kph;
@@ -490,18 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
             kp.x = a2.x, kp.y = a2.y, vp.x = b2.x, vp.y = b2.y;
           }
         }
-        // ---- the tile's exponents: of the largest scale or low of its keys, of its values
+        // ---- the tile's units: one for its keys, one for the values of each group
         uint32_t ka = 0, va = 0;
         const uint32_t pk[4] = {kp.x, kp.y, kp.z, kp.w}, pv[4] = {vp.x, vp.y, vp.z, vp.w};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const uint32_t a = pk[g] & 0x7FFFu, b = (pk[g] >> 16) & 0x7FFFu;
-          const uint32_t c = pv[g] & 0x7FFFu, d = (pv[g] >> 16) & 0x7FFFu;
-          ka = max(ka, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
-          va = max(va, max(c < 0x7F80u ? c : 0u, d < 0x7F80u ? d : 0u));
+          ka = max(ka, reach(pk[g]));
+          va |= __reduce_max_sync(0xFFFFFFFFu, reach(pv[g]) >> 7) << (8 * g);
         }
-        ka = __reduce_max_sync(0xFFFFFFFFu, ka);
-        va = __reduce_max_sync(0xFFFFFFFFu, va);
+        ka = __reduce_max_sync(0xFFFFFFFFu, ka >> 7);
         uint32_t* mx = s_max + (n & 1) * 8;
         if (lane == 0) {
           mx[(warp - 8) * 2] = ka;
@@ -509,12 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         }
         out = bar_red_or(1, 128, !ok);
         if (out) break;
-        ka = max(max(mx[0], mx[2]), max(mx[4], mx[6]));
-        va = max(max(mx[1], mx[3]), max(mx[5], mx[7]));
-        const uint32_t ke = max(ka >> 7, 47u);
-        ve = max(ve, va >> 7);
-        // scales and lows below 2^-8: times 2^-(e + 9)
-        const int kn = (int)ke - 127 + 9, vn = (int)ve - 127 + 9;
+        const uint32_t ke = max(max(max(mx[0], mx[2]), max(mx[4], mx[6])), 47u);
+        ve = __vmaxu4(ve, __vmaxu4(__vmaxu4(mx[1], mx[3]), __vmaxu4(mx[5], mx[7])));
+        const int kn = (int)ke - 118;  // scales below 2^-8: times 2^-(e + 9), e = ke - 127
         const uint32_t on = __ballot_sync(0xFFFFFFFFu, pg != -2);
         if (pg == -2) kv4_record(p.a.b.status);
         // ---- K(n), once S(n - 2) has been taken of its buffer
@@ -523,14 +544,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           Info& in = info[n & 3];
           if (tok == 0) {
             // in two factors: 2^kn alone, or with a small f, may leave fp32's range
-            in.k_unit[0] = exp2f((float)(kn >> 1));
-            in.k_unit[1] = exp2f((float)(kn - (kn >> 1)));
-            in.v_exp = vn;
+            in.k_unit[0] = pow2(kn >> 1);
+            in.k_unit[1] = pow2(kn - (kn >> 1));
+            in.v_exp = ve;
           }
           if (lane == 0) in.on[warp - 8] = on;
           unsigned char* dst = smem + C::kOffK + (n & 1) * C::kTileBytes;
           // 2^(24 - kn), in two factors (either may leave fp32's range alone)
-          const float a0 = exp2f((float)((24 - kn) >> 1)), a1 = exp2f((float)(24 - kn - ((24 - kn) >> 1)));
+          const float a0 = pow2((24 - kn) >> 1), a1 = pow2(24 - kn - ((24 - kn) >> 1));
           __half2 se[NG], so[NG], lo[NG];
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
@@ -562,10 +583,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
         }
         if (ok) {
           unsigned char* dst = smem + C::kOffV + (n & 1) * C::kTileBytes;
-          const float a0 = exp2f((float)((24 - vn) >> 1)), a1 = exp2f((float)(24 - vn - ((24 - vn) >> 1)));
           float sc[NG], lw[NG];
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
+            const int e = 24 - unit_exp(ve, g);
+            const float a0 = pow2(e >> 1), a1 = pow2(e - (e >> 1));
             sc[g] = __uint_as_float(pv[g] << 16) * a0 * a1;
             lw[g] = __uint_as_float(pv[g] & 0xFFFF0000u) * a0 * a1 * 0x1p-24f;
             // a NaN group stands as 0 in the products (rows that do not see the token must not

@@ -543,10 +543,16 @@ size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
  * 0.  Listed blocks outside the sequence, pages outside the cache, and rows out
  * of range are skipped (o is 0 there) and reported as SBSA_ERR_DEVICE; a
  * repeated block is attended twice.
- * Precision: products in fp16 with fp32 accumulation, exact up to the rounding of the
- * weights (2^-11 of each; fp32 rows take both operands in two parts, 2^-22) and, for
- * more than 48 (d = 64) or 32 (d = 128) rows of a kv head, of the dequantised keys and values
- * (2^-11).  Results do not change between runs.
+ * Precision: products in fp16 with fp32 accumulation; softmax and sums in fp32.  Beside that:
+ *   up to 48 (d = 64) or 32 (d = 128) rows of a kv head (max_new * Hq / Hkv), fp32 or lists:
+ *     a weight times a value's scale is rounded by 2^-11 of it, or by 2^-31 of the largest
+ *     weight times the largest scale or low that the row has met, whichever is more (fp32 rows
+ *     take both operands in two parts: 2^-22); bf16 rows' sums of products keep 18 bits.
+ *   more rows (bf16, no lists): a weight is rounded by 2^-11 of it or 2^-25 of the row's
+ *     largest; a key by 2^-11 of it or 2^-15 of the largest scale within 128 tokens, a value by
+ *     2^-11 of it or 2^-15 of the largest scale of its group of 32 channels so far (2^-37 of
+ *     the largest low where that is above 2^22 scales), whichever is more.
+ * Results do not change between runs.
  * Errors as sbsa_kv4_append, SBSA_ERR_UNSUPPORTED also for n_tokens * Hq or n_seqs * Hq
  * above 2^31 - 2^16, and SBSA_ERR_WORKSPACE for a missing, misaligned or short
  * workspace.

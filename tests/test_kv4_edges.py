@@ -196,3 +196,45 @@ def test_rows_that_the_tensors_do_not_have(kv4, cuda, new, first, last):
     want, size, span = KP.attend(decoded, q.float().cpu().numpy(), b.table, b.lens, b.cu)
     err = np.abs(out.float().cpu().numpy() - want[:, lo:hi])
     assert (err <= _tolerance(want, size, span, "bf16", 300, d)[:, lo:hi]).all()
+
+
+# ------------------------------------------------------------------------- groups and weights far apart
+
+def _spans(b, hq, seq=0):
+    """[Hq, T, d / 32]: the largest |value| of each group that a row sees, and [Hq, 1, d / 32] the largest scale."""
+    n, new = b.lens[seq], b.new[seq]
+    v = np.abs(KP.tokens(KP.decode(b.cache), b.table[seq], n)[1])            # [n, Hkv, d]
+    most = np.maximum.accumulate(v.reshape(n, b.hkv, -1, 32).max(-1), 0)[n - new:]
+    scale = np.stack([[(_token(b, seq, pos, 1, h)[1][:, 0].astype(np.uint32) << 16).view(np.float32)
+                       for h in range(b.hkv)] for pos in range(n)]).max(0)
+    share = hq // b.hkv
+    return most.transpose(1, 0, 2).repeat(share, 0).astype(np.float64), scale[:, None].repeat(share, 0).astype(np.float64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 16, 70])
+def test_groups_of_different_magnitude(kv4, cuda, d, new):
+    """Values whose groups differ by 2^11 (few rows) and 2^24 (many): each group to its own precision, 2^-11 of
+    its largest value for the weights and as much for the values.  Beside that, few rows: a weight times a
+    scale is rounded to 2^-31 of the largest value's magnitude at least, and multiplies at most 8; many rows: a
+    value to 2^-15 of its group's largest scale."""
+    rng = np.random.default_rng(new + d)
+    n, hkv, hq = 300 + new, 1, 2
+    many = new * hq > 48
+    b = _fast_fill(Batch([n], [new], 32, hkv, d, seed=5), rng)
+    power = np.array([0, -20, 4, -9] if many else [0, -10, 1, -5])[:d // 32]
+    for pos in range(n):
+        p = _token(b, 0, pos, 1, 0)[1]
+        f = (p.astype(np.uint32) << 16).view(np.float32) * (2.0 ** (power + rng.integers(-1, 2)))[:, None].astype(np.float32)
+        p[:] = f.view(np.uint32) >> 16
+    b.gpu()
+    q = _rows(rng, hq, new, d, "bf16", True, 1.2)
+    out = kv4.attend(b.g_cache, q, *b.g, new)
+    assert _status(kv4) == 0
+    want, size, _ = KP.attend(KP.decode(b.cache), q.float().cpu().numpy(), b.table, b.lens, b.cu)
+    span, scale = _spans(b, hq)
+    floor = 2.0 ** -15 * scale if many else n * 8 * 2.0 ** -31 * span.max() * np.ones_like(scale)
+    tol = (2.0 ** -11 * span * (2 + 2 * size) + floor).repeat(32, -1) + 2.0 ** -8 * np.abs(want)
+    err = np.abs(out.float().cpu().numpy() - want)
+    assert (err <= tol).all(), ((err / tol).reshape(hq, new, -1, 32).max((0, 1, 3)))
