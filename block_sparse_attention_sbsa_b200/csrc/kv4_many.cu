@@ -60,8 +60,12 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kRows = 256;  // of an item: two tiles of 128
 constexpr int kItemCost = 5;
 constexpr int kThreads = 512;
-// 256 * 152 + 128 * 128 + 128 * 80 = 512 * 128, what the block is launched with
-constexpr int kRegsSoftmax = 152, kRegsUnpack = 128, kRegsIssue = 80;
+// What the block is launched with, 512 * 128, divided anew.  The issuing thread's loop spills below 96
+// (88: 150 bytes, 80: 230, 72: 500), which shows in every token tile.
+constexpr int kRegsSoftmax = 144, kRegsUnpack = 128, kRegsIssue = 96;
+static_assert(256 * kRegsSoftmax + 128 * (kRegsUnpack + kRegsIssue) <= kThreads * 128 && kRegsSoftmax >= 128 &&
+                  kRegsUnpack <= 128 && kRegsIssue <= 128,
+              "the softmax warps' share is raised from 128, the others' are lowered");
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLeastFactor = 0x1p-126f, kMostFactor = 0x1p80f;  // (|S'| is below 2^32)
 

@@ -121,16 +121,21 @@ struct Seq {
 };
 
 __device__ __forceinline__ Seq seq_of(const SplitParams& p, int b) {
-  Seq s;
   // the rows that the tensors have; positions go by cu and the length as they are given
-  const int from = p.a.b.cu[b], to = p.a.b.cu[b + 1], len = p.a.b.lens[b];
-  const int lo = clamp_int(from, 0, p.a.b.n_tokens), hi = clamp_int(to, lo, p.a.b.n_tokens);
-  if (lo != from || hi != to) kv4_record(p.a.b.status);
-  kv4_named(p.a.b, len);
-  s.first = lo;
-  s.rows = hi - lo;
-  s.ahead = (int)max((long long)len - to + lo, -0x7FFF0000LL);
+  const int to = p.a.b.cu[b + 1];
+  Seq s;
+  s.first = clamp_int(p.a.b.cu[b], 0, p.a.b.n_tokens);
+  s.rows = clamp_int(to, s.first, p.a.b.n_tokens) - s.first;
+  // (31 bits hold it for a sequence with rows: to > first >= 0; a negative length is as good as none)
+  s.ahead = (int)((uint32_t)max(p.a.b.lens[b], 0) - (uint32_t)to + (uint32_t)s.first);
   return s;
+}
+
+// Reports a sequence that is longer than the table, or whose rows the tensors do not have.
+__device__ __forceinline__ void check_seq(const SplitParams& p, int b) {
+  const int from = p.a.b.cu[b], to = p.a.b.cu[b + 1];
+  kv4_named(p.a.b, p.a.b.lens[b]);
+  if (from < 0 || to < from || to > p.a.b.n_tokens) kv4_record(p.a.b.status);
 }
 
 // Row `row` of the item head: the token row, its number in the sequence and the
@@ -145,6 +150,10 @@ __device__ __forceinline__ bool row_of(const SplitParams& p, const Seq& s, int h
   return true;
 }
 
+// The kernel for many rows is not called with lists.
+template <int ROWS>
+constexpr bool kTakesLists = ROWS <= 16;
+
 // The items of one (sequence, head).  (Rows times heads fit 31 bits: checked on the host.)
 template <int ROWS>
 struct Items {
@@ -157,7 +166,7 @@ struct Items {
     seq = seq_of(p, b);
     tiles = (int)(((uint32_t)seq.rows * (uint32_t)p.group + ROWS - 1) / ROWS);
     listed = -1;
-    if (p.a.list_heads) {
+    if (kTakesLists<ROWS> && p.a.list_heads) {
       const int n = clamp_int(p.a.cnt[(long long)b * p.heads + head], 0, p.a.max_blocks);
       listed = (n * p.a.block + kSplitUnit - 1) / kSplitUnit;
     }
@@ -169,7 +178,7 @@ struct Items {
   }
   // Units of a tile; one that sees nothing still takes one (it writes zeros).
   __device__ int units(const SplitParams& p, int tile) const {
-    const int n = listed >= 0 ? listed : (limit(p, tile) + kSplitUnit - 1) / kSplitUnit;
+    const int n = kTakesLists<ROWS> && listed >= 0 ? listed : (limit(p, tile) + kSplitUnit - 1) / kSplitUnit;
     return n < 1 ? 1 : n;
   }
   template <int COST>
@@ -201,8 +210,10 @@ __device__ __forceinline__ bool split_run(const SplitParams& p, long long* s_sca
   const int per = (items + THREADS - 1) / THREADS;
   const int i0 = min(items, (int)threadIdx.x * per), i1 = min(items, i0 + per);
   long long mine = 0;
-  for (int i = i0; i < i1; ++i)
+  for (int i = i0; i < i1; ++i) {
     mine += Items<ROWS>(p, i / p.heads, i % p.heads).template cost<COST>(p);
+    if (blockIdx.x == 0 && i % p.heads == 0) check_seq(p, i / p.heads);
+  }
   long long incl = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
