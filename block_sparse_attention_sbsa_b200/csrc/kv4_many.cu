@@ -67,6 +67,9 @@ static_assert(256 * kRegsSoftmax + 128 * (kRegsUnpack + kRegsIssue) <= kThreads 
                   kRegsUnpack <= 128 && kRegsIssue <= 128,
               "the softmax warps' share is raised from 128, the others' are lowered");
 constexpr float kRescaleLog2 = 8.0f;
+// Weights are 2^(logit - m + kHeadLog2), m a reference that the logits outgrow by 2^8 at most: below
+// 2^15 in fp16, and those down to 2^-21 of the largest are normal numbers.
+constexpr float kHeadLog2 = 7.0f;
 constexpr float kLeastFactor = 0x1p-126f, kMostFactor = 0x1p80f;  // (|S'| is below 2^32)
 
 constexpr int kHalves = 3;
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(const __grid_cons
           }
         }
         // (two at a time: packed fp32 operations halve what is issued for all but the exponentials)
-        const uint64_t c2 = pack2(c, c), m2 = pack2(-m, -m);
+        const uint64_t c2 = pack2(c, c), m2 = pack2(kHeadLog2 - m, kHeadLog2 - m);
         uint64_t sum = pack2(0.f, 0.f);
         // the weights; PV of the first 64 tokens may begin while the others are at work
 #pragma unroll 1

@@ -548,7 +548,7 @@ size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
  *     a weight times a value's scale is rounded by 2^-11 of it, or by 2^-31 of the largest
  *     weight times the largest scale or low that the row has met, whichever is more (fp32 rows
  *     take both operands in two parts: 2^-22); bf16 rows' sums of products keep 18 bits.
- *   more rows (bf16, no lists): a weight is rounded by 2^-11 of it or 2^-25 of the row's
+ *   more rows (bf16, no lists): a weight is rounded by 2^-11 of it or 2^-32 of the row's
  *     largest; a key by 2^-11 of it or 2^-15 of the largest scale within 128 tokens, a value by
  *     2^-11 of it or 2^-15 of the largest scale of its group of 32 channels so far (2^-37 of
  *     the largest low where that is above 2^22 scales), whichever is more.

@@ -238,3 +238,35 @@ def test_groups_of_different_magnitude(kv4, cuda, d, new):
     tol = (2.0 ** -11 * span * (2 + 2 * size) + floor).repeat(32, -1) + 2.0 ** -8 * np.abs(want)
     err = np.abs(out.float().cpu().numpy() - want)
     assert (err <= tol).all(), ((err / tol).reshape(hq, new, -1, 32).max((0, 1, 3)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [70, 300])
+def test_weights_far_below_the_largest(kv4, cuda, d, new):
+    """Many rows: a token that takes nearly all of the weight and whose value is 0, before 4096 tokens of 2^-22.7
+    of its weight each, so that the output is theirs; in 148 sequences on the same pages, so that each is
+    about one CTA's.  Keys are constant groups: the logits are exact but for their own roundings in the
+    exponentials' arguments (2^-24 of 23, twice).  A weight is kept to half a step of fp16 denormals beside a
+    largest one of 2^7, so to 2^-25 of 2^-15.7; a value to 2^-11 of it and 2^-15 of its scale."""
+    others, seqs = 4096, 148
+    top = {128: 1.390625, 64: 1.96875}[d]                    # sqrt(d) * top * log2(e) = 22.7
+    n = 1 + others + new
+    rng = np.random.default_rng(new)
+    b = _fast_fill(Batch([n], [new], 128, 1, d, seed=9), rng)
+    rec = b.cache.reshape(b.pages, 1, 2, -1)
+    rec[:, :, 0] = 0
+    pair = np.array([1.0 / 16, 1.0], np.float32).view(np.uint32) >> 16
+    rec[:, :, 1, b.page * d // 2:] = np.tile(pair.astype(np.uint16).view(np.uint8), (b.pages, 1, b.page * d // 32))
+    _constant(b, 0, 0, 0, top)
+    _constant(b, 0, 0, 1, 0.0)
+    b.gpu()
+    table, lens = b.g[0].repeat(seqs, 1), b.g[1].repeat(seqs)
+    cu = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * new
+    q = torch.ones(1, seqs * new, d, dtype=torch.bfloat16, device="cuda")
+    out = kv4.attend(b.g_cache, q, table, lens, cu, new)
+    assert _status(kv4) == 0
+    want = KP.attend(KP.decode(b.cache), q[:, :new].float().cpu().numpy(), b.table, b.lens, b.cu)[0]
+    err = np.abs(out.float().cpu().numpy().reshape(seqs, new, d) - want)
+    rel = 2.0 ** -8 + 2.0 ** -9.3 + 2.0 ** -11 + 2.0 ** -15 + 2.0 ** -18
+    assert (err <= rel * np.abs(want)).all(), (err / np.abs(want)).max()
