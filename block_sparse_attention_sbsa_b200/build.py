@@ -27,7 +27,7 @@ SOURCES = ["pool.cu", "select.cu", "score_rowmax.cu", "score_centroid.cu", "atte
            "sbsa_noalloc.cu",
            "kv4_api.cu", "kv4_cache.cu", "kv4_few.cu", "kv4_many.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "tma_map.h", "kv4.h", "kv4.cuh",
-           "kv4_split.cuh"]
+           "kv4_split.cuh", "kv4_ready.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -30,7 +30,8 @@
 // partial results.  Of an item shared by several CTAs each leaves its part in the
 // workspace, and the one that has its last unit joins them when it is done with its own
 // run: it waits only for CTAs before it, which wait for nobody before they have left their
-// parts.  (A second kernel for the joins cost a launch on the host, and on the GPU: 33 listed
+// parts; after a failure (a wait that ran out) nothing is joined, and the words that say what
+// is there are left clean (kv4_ready.h).  (A second kernel for the joins cost a launch on the host, and on the GPU: 33 listed
 // blocks of 8 sequences 24.6 us, 23.0 without; 524288 tokens 164, 159 at the time.)  Everything is in
 // a fixed order: results do not change between runs.
 #include <cuda_fp16.h>
@@ -41,6 +42,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "kv4_ready.h"
 #include "kv4_split.cuh"
 #include "ptx.cuh"
 #include "tma_map.h"
@@ -195,6 +197,24 @@ __device__ __forceinline__ void load_q8(const float* p, float (&x)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
+// A word of kv4_ready.h in the workspace.
+struct ReadyWord {
+  uint64_t* at;
+  __device__ uint64_t load() const {
+    uint64_t x;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(at) : "memory");
+    return x;
+  }
+  __device__ uint64_t exchange(uint64_t x) const {
+    uint64_t old;
+    asm volatile("atom.exch.acq_rel.gpu.global.b64 %0, [%1], %2;" : "=l"(old) : "l"(at), "l"(x) : "memory");
+    return old;
+  }
+  __device__ void store(uint64_t x) const {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(x) : "memory");
+  }
+};
+
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -760,8 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
         join_seq = s, join_head = w.head, join_row0 = row0, join_first = w.first_cta(run);
       } else {
         consumers_sync<kWarps * 32>();
-        if (threadIdx.x == 0)
-          asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.ready + slot), "l"(p.call) : "memory");
+        if (threadIdx.x == 0) ready_publish(ReadyWord{p.ready + slot}, p.call, *abort_flag != 0);
       }
     }
   }
@@ -771,20 +790,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attend_kernel(const __grid_co
   const int others = cta - join_first;
   auto slot_of = [&](int k) { return k == 0 ? 2 * join_first + 1 : 2 * (join_first + k); };
   if ((int)threadIdx.x < others) {
+    const ReadyWord word{p.ready + slot_of(threadIdx.x)};
     const uint64_t t0 = global_timer_ns();
-    while (ok) {
-      uint64_t x;
-      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(p.ready + slot_of(threadIdx.x)) : "memory");
-      if (x == p.call) break;
-      if (*abort_flag || global_timer_ns() - t0 > kTimeoutNs) ok = false;
-    }
+    Ready found = kReadyNot;
+    while (ok && (found = ready_look(word, p.call)) == kReadyNot)
+      ok = !*abort_flag && global_timer_ns() - t0 <= kTimeoutNs;
+    ready_leave(word, p.call, found == kReadyNot);
+    ok = found == kReadyPart;
   }
   if (bar_red_or(1, kWarps * 32, !ok)) {
     if (threadIdx.x == 0 && !*abort_flag) fail();
     return;
   }
-  // for a replay of this call in a graph
-  if ((int)threadIdx.x < others) p.ready[slot_of(threadIdx.x)] = 0;
   // the warps take the parts (the last one is this CTA's) in turn, and join like after an item
   constexpr int kPerRow = D / 4;              // lanes of a row, 4 channels each
   constexpr int kRowsWarp = 32 / kPerRow;     // rows of a warp's pass

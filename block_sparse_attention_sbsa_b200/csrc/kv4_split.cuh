@@ -50,19 +50,19 @@ struct SplitParams {
   float* slots;      // two a CTA: of the item that begins before its run, and of the one that
                      // goes on behind it
   Part* parts;       // one a CTA
-  uint64_t* ready;   // one a slot: `call` once the slot holds its part (see kv4_few.cu)
+  uint64_t* ready;   // one a slot (kv4_ready.h)
   uint64_t call;
 };
 
 // A number that no other call has (and that memory which no call has written does not hold by
-// chance).
+// chance); it ends in binary 01.
 inline uint64_t call_number() {
   static std::atomic<uint64_t> next{
       (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count()};
   uint64_t z = (next.fetch_add(1) + 1) * 0x9E3779B97F4A7C15ull;  // splitmix64 (Steele, Lea, Flood)
   z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
   z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
-  return (z ^ (z >> 31)) | 1;
+  return ((z ^ (z >> 31)) & ~3ull) | 1;
 }
 
 inline SplitParams split_params(const Kv4AttendArgs& a, int slot_rows) {

@@ -2,6 +2,8 @@
 rows beyond what a table or a tensor holds, groups of different magnitude, weights far below the
 largest, replays of captured graphs.  Tolerances as in test_kv4.py, plus what stands at a test.
 """
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -270,3 +272,81 @@ def test_weights_far_below_the_largest(kv4, cuda, d, new):
     err = np.abs(out.float().cpu().numpy().reshape(seqs, new, d) - want)
     rel = 2.0 ** -8 + 2.0 ** -9.3 + 2.0 ** -11 + 2.0 ** -15 + 2.0 ** -18
     assert (err <= rel * np.abs(want)).all(), (err / np.abs(want)).max()
+
+
+# ------------------------------------------------------- CPU: the words that hand over partial results
+
+READY = r'''
+#include <cstdint>
+#include <cstdio>
+#include <functional>
+#include "kv4_ready.h"
+using namespace sbsa;
+// One word, and what the other side does between two accesses of this side (once).
+struct Word {
+  uint64_t* at;
+  std::function<void()>* between;
+  void step() const {
+    if (between && *between) {
+      auto f = *between;
+      *between = nullptr;
+      f();
+    }
+  }
+  uint64_t load() const { return *at; }
+  uint64_t exchange(uint64_t x) const {
+    const uint64_t old = *at;
+    *at = x;
+    step();
+    return old;
+  }
+  void store(uint64_t x) const { *at = x; }
+};
+int main() {
+  const uint64_t call = 0x123456789ABCDEF1ull, other = 0x0F0F0F0F0F0F0F05ull;
+  int bad = 0;
+  auto is = [&](bool good, const char* what, int order, int failed) {
+    if (!good) ++bad, printf("%s: order %d, failed %d\n", what, order, failed);
+  };
+  const uint64_t held[] = {0, other, other + 1, other + 2, ~(uint64_t)0, call + 4};
+  for (uint64_t before : held)
+    for (int failed = 0; failed < 2; ++failed) {
+      uint64_t word = before;
+      const Word w{&word, nullptr};
+      // an ordinary call: nothing there, then there, then cleared
+      is(ready_look(w, call) == kReadyNot, "nothing yet", 0, failed);
+      ready_publish(w, call, failed != 0);
+      is(ready_look(w, call) == (failed ? kReadyFailed : kReadyPart), "published", 0, failed);
+      ready_leave(w, call, false);
+      is(word == 0, "left as 0", 0, failed);
+      // a joiner that gives up, before, after and in the middle of publishing: no later run of the same
+      // call (a replay) may find a part, nor a joiner that has gone
+      for (int order = 0; order < 4; ++order) {
+        word = before;
+        std::function<void()> none, leave = [&] { ready_leave(Word{&word, nullptr}, call, true); },
+                              publish = [&] { ready_publish(Word{&word, nullptr}, call, failed != 0); };
+        if (order == 0) publish(), leave();
+        if (order == 1) leave(), publish();
+        if (order == 2) ready_publish(Word{&word, &leave}, call, failed != 0);
+        if (order == 3) ready_leave(Word{&word, &publish}, call, true);
+        is(ready_look(w, call) == kReadyNot, "after giving up", order, failed);
+        ready_publish(w, call, false);
+        is(ready_look(w, call) == kReadyPart, "the next run", order, failed);
+        ready_leave(w, call, false);
+        is(word == 0, "the next run's end", order, failed);
+      }
+    }
+  return bad != 0;
+}
+'''
+
+
+def test_words_of_shared_items_are_clean_after_a_failure(tmp_path):
+    """A partial result's word, in every order of the CTA that leaves the part and the one that takes it or
+    gives up: afterwards it holds nothing that the same call, replayed in a graph, would take for a part."""
+    import block_sparse_attention_sbsa_b200.build as build
+    src, exe = tmp_path / "ready.cpp", tmp_path / "ready"
+    src.write_text(READY)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", build.CSRC, "-o", str(exe), str(src)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
