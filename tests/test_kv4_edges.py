@@ -274,6 +274,60 @@ def test_weights_far_below_the_largest(kv4, cuda, d, new):
     assert (err <= rel * np.abs(want)).all(), (err / np.abs(want)).max()
 
 
+# ------------------------------------------------------------------------------ captured and replayed
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d,new", [(8, 2, 128, 70), (4, 2, 64, 150), (8, 2, 64, 3)])
+def test_replays_share_out_the_tokens_anew(kv4, cuda, hq, hkv, d, new):
+    """Two graphs on one workspace, with append and the attention of many rows (and of few), replayed in turn with
+    other lengths and numbers of rows: contexts that all CTAs share, that some share, that none shares, and
+    sequences without a row; also on a stream of its own, and with other memory in the workspace between."""
+    rng = np.random.default_rng(new)
+    page, most = 64, 5000
+    b = _fast_fill(Batch([most, most], [new, new], page, hkv, d, seed=8), rng).gpu()
+    k, v = (_rows(rng, hkv, b.total, d, "bf16", True) for _ in range(2))
+    q = _rows(rng, hq, b.total, d, "bf16", True, 1.5)
+    p = kv4.Params(hq, hkv, d, page, b.pages, b.table.shape[1], 2, b.total, new, 0)
+    size = kv4.attend_workspace_bytes(p)
+    assert size > 0
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    kv4.append(b.g_cache, k, v, *b.g)
+    kv4.attend(b.g_cache, q, *b.g, new, out=outs[0], workspace=ws)
+    graphs = []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kv4.append(b.g_cache, k, v, *b.g)
+            kv4.attend(b.g_cache, q, *b.g, new, out=o, workspace=ws)
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    for step, (lens, rows) in enumerate((([most, 700], [new, new]), ([new, 1], [new, 1]), ([3000, 129], [0, 1]),
+                                         ([most, most], [new, 2]), ([128, 77], [min(new, 128), 1]),
+                                         ([1411, 3001], [new // 2, new]))):
+        b.lens, b.new, b.cu = lens, rows, np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        b.g[1].copy_(torch.tensor(lens, dtype=torch.int32))
+        b.g[2].copy_(torch.from_numpy(b.cu))
+        for x, heads in ((q, hq), (k, hkv), (v, hkv)):
+            x.copy_(_rows(rng, heads, b.total, d, "bf16", True, 1.5))
+        ws.fill_(step * 51)
+        for o in outs:
+            o.fill_(3.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side if step % 2 else torch.cuda.current_stream()):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        xk, xv = k.float().cpu().numpy(), v.float().cpu().numpy()
+        for s, n in enumerate(lens):
+            for t in range(b.cu[s], b.cu[s + 1]):
+                b.put(s, n - b.cu[s + 1] + t, xk[:, t], xv[:, t])
+        assert _status(kv4) == 0
+        for o in outs:
+            _check(kv4, b, q, o, torch.full_like(q, 3.0))
+    del graphs
+
+
 # ------------------------------------------------------- CPU: the words that hand over partial results
 
 READY = r'''
