@@ -78,8 +78,11 @@ Kv4Batch batch(const sbsa_kv4_params* p, const int32_t* table, const int32_t* le
 
 // Which kernel: the one for many rows reads the cache once for 256 rows, the other one for
 // 16, but spends less on what it reads, so that it takes up to two reads (d = 128) or three
-// (d = 64) to equal it.  12 sequences of 907 to 20011 tokens, 8 kv heads, d = 128: 32 rows few
-// 82 us, many 109; 33 to 48 rows 115 and 109.  d = 64: 33 to 48 rows 81 and 92.
+// (d = 64) to equal it.  12 sequences of 907 to 20011 tokens, 8 kv heads, all with the same number
+// of rows (bursts of 10 ms, in a graph): d = 128, 32 rows few 81 us, many 111, 36 to 48 rows 115 and
+// 111; d = 64, 40 and 48 rows 79 and 92, 52 rows 102 and 92.  The host knows max_new alone, so one
+// chunk takes a batch's single tokens along: 47 of them over 211 to 16411 tokens with a chunk of 512
+// over 8192, d = 128, are 334 us in one call (many), 190 in two.
 bool many_rows(const sbsa_kv4_params* p) {
   return p->dtype == SBSA_BF16 && !p->list_heads &&
          (long long)p->max_new * (p->n_q_heads / p->n_kv_heads) > (p->head_dim == 64 ? 48 : 32);

@@ -12,8 +12,9 @@
 // mantissa of 2^23, the place in the word going into the scale.  A CTA takes a tile of
 // tokens of one kv head and side.  append collects the tile's rows in shared memory and
 // writes them to the pages 16 bytes a thread, token after token, whatever the order of the
-// inputs.  Measured: the 128k prompt 122 us (5.8 TB/s, 0.88 of a copy; 256 with a thread for 8
-// channels), a 32k context read in 32 us (5.5 TB/s; 49 with 4 bytes a thread).
+// inputs.  Measured among other calls for a second: the 128k prompt 136 us (5.2 TB/s, 0.79 of a
+// copy), a 32k context read in 32.8 us (5.4 TB/s, 0.82); in bursts of 12 ms, before the power limit
+// lowers the clocks, 120 us (256 with a thread for 8 channels) and 31 (49 with 4 bytes a thread).
 #include <cuda_runtime.h>
 
 #include "kv4.cuh"

@@ -12,8 +12,9 @@
 //
 // Bound: HBM, 5/4 d bytes a token and kv head.  At 6.5 TB/s an SM has about
 // 110 cycles for 16 tokens (d = 128, 2560 bytes), and the work on them is
-// about 350 warp instructions (88 issue cycles) at 8 rows and takes 150 cycles (524288 tokens of 8
-// kv heads, 64 query heads: 153 us, 4.4 TB/s; without the arithmetic 122): levels must be
+// about 370 warp instructions (93 issue cycles) at 8 rows and takes 155 cycles (524288 tokens of 8
+// kv heads, 64 query heads: 163 us, 4.1 TB/s, among other calls for a second; in bursts of 12 ms,
+// before the power limit lowers the clocks, 152, and without the arithmetic 122): levels must be
 // unpacked with next to nothing, which rules out a copy in fp16 through shared
 // memory for tcgen05 (its writes and reads alone would exceed the shared memory's
 // bandwidth).  The products therefore run on mma.sync m16n8k16, whose

@@ -17,7 +17,10 @@
 // Bound: the tensor cores and the exponentials alike.  A tile of 128 tokens against 256
 // rows is 2 * 2 * 2^21 multiply-adds, 2096 cycles at 4000 a cycle, its 2^15 exponentials
 // 2048 cycles at 16 a cycle.  Neither is reached: 4096 new of 32768 tokens, 32 query heads on 8,
-// 2.05 ms (1005 TFLOP/s, 0.61 of cuBLAS; 2.00 to 2.11), about 4,400 cycles a token tile: softmax
+// 2.26 ms among other calls for a second (912 TFLOP/s, 0.66 of what cuBLAS holds that long: the
+// power limit lowers the clocks); in bursts of 12 ms 2.07 ms (998 TFLOP/s, 0.60 of cuBLAS's burst).
+// The parts below were measured in short runs on the form that took 2.00 to 2.05 (one unit for
+// all groups of the values): about 4,400 cycles a token tile, softmax
 // 2,700 of them and 1,500 of waiting for the products, unpacking 3,300 and 1,100 of waiting.  No
 // single role is what the others wait for: without the exponentials 2.00 ms, without the unpacking
 // loops 1.86, with a quarter of the products 1.91.  (S in halves of 64 tokens, so that softmax and
@@ -25,9 +28,10 @@
 // bytes a cycle of shared memory: 3.3 ms, with an issuing thread for each query tile 2.1.)
 // Four roles at a time share the instruction caches, so their loops are kept short (unroll 1 where
 // it stands): all unrolled, 2.5 of the 12 warp cycles that an issued instruction cost were spent
-// waiting for instructions (now 0.44 of 8.4) and the same call took 2.78 ms; with the unpacking
-// loops short 2.25.  The softmax reads S twice out of TMEM, 64 columns at a time, for the same
-// reason, and then needs so few registers that hardly anything spills (2.05).
+// waiting for instructions (then 0.44 of 8.4, now 0.65) and the same call took 2.78 ms; with the
+// unpacking loops short 2.25.  The softmax reads S twice out of TMEM, 64 columns at a time, for the
+// same reason, and then needs so few registers that hardly anything spills (2.05).  How the
+// compiler lays the roles out is worth up to 5 % of it either way.
 //
 // One CTA an SM, 16 warps:
 //   0-3, 4-7  softmax of tile A, of tile B: a thread has a row; S out of TMEM, P (fp16)

@@ -185,7 +185,8 @@ def read(cache, page_table, seq_lens, cu_new, k_out=None, v_out=None, stream=Non
 def attend(cache, q, page_table, seq_lens, cu_new, max_new: int, idx=None, cnt=None,
            block_size: int = 0, sm_scale: float = 0.0, out=None, workspace=None, stream=None):
     """o [Hq, n_tokens, d] (into `out` when given) of causal attention of the rows q over the
-    cache, which holds their own tokens already.  max_new: at least the most rows of one sequence.
+    cache, which holds their own tokens already.  max_new: at least the most rows of one sequence
+    (it chooses the kernel for the whole call: single tokens and a prompt's chunk are faster apart).
     idx [n_seqs, heads, max_blocks] and cnt [n_seqs, heads] (heads = Hkv or Hq) restrict it to the
     listed blocks of block_size tokens.  workspace: uint8, at least attend_workspace_bytes
     (allocated when None)."""

@@ -537,6 +537,8 @@ size_t sbsa_kv4_attend_workspace_bytes(const sbsa_kv4_params* p);
  *   workspace device, 256-byte aligned, ws_bytes >= sbsa_kv4_attend_workspace_bytes(p);
  *             nothing in it is kept between calls.  Calls that may overlap on
  *             the GPU need one each.
+ * max_new chooses how the call is computed (few or many rows of a kv head, see Precision), for all
+ * of its sequences: many single tokens together with a chunk of a prompt are faster in two calls.
  * o of row t (token position n of sequence b) = sum over the tokens u <= n, of
  * the listed blocks if there are lists, of softmax_u(q . K[u] * sm_scale) V[u],
  * where query head h reads kv head h / (Hq / Hkv); a row that sees no token is
