@@ -32,9 +32,9 @@
 // workspace, and the one that has its last unit joins them when it is done with its own
 // run: it waits only for CTAs before it, which wait for nobody before they have left their
 // parts; after a failure (a wait that ran out) nothing is joined, and the words that say what
-// is there are left clean (kv4_ready.h).  (A second kernel for the joins cost a launch on the host, and on the GPU: 33 listed
-// blocks of 8 sequences 24.6 us, 23.0 without; 524288 tokens 164, 159 at the time.)  Everything is in
-// a fixed order: results do not change between runs.
+// is there are left clean (kv4_ready.h).  (A second kernel for the joins cost a launch on the
+// host, and on the GPU: 33 listed blocks of 8 sequences 24.6 us, 23.0 without; 524288 tokens
+// 164, 159 at the time.)  Everything is in a fixed order: results do not change between runs.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
